@@ -467,3 +467,9 @@ def _ceiling():
         lib_c.bsq_ceiling_expand.restype = _i32
         _ceiling_lib = lib_c
     return _ceiling_lib
+
+
+# the serving operators: 8-bit KV cache, its pages, mixture of experts for a few tokens
+from .serving import (KV_PAGE, KvCache, kv_cache, kv_cache_append, kv_cache_attention,  # noqa: E402
+                      kv_pages_compact, kv_pages_copy, kv_pages_fork, kv_pages_free,
+                      kv_pages_reserve, moe_few_tokens, serving_lib)

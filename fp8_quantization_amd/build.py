@@ -1,4 +1,4 @@
-"""Build ``libbsq.so`` in-tree with hipcc for gfx950.
+"""Build ``libbsq.so``, ``libbsq_serving.so`` and ``libbsq_ceiling.so`` in-tree with hipcc for gfx950.
 
 Flags that matter for bit-exact results:
   -ffp-contract=off                          no fused multiply-adds are formed
@@ -21,6 +21,10 @@ SOURCES = [os.path.join(CSRC, "bsq_api.cpp"), os.path.join(CSRC, "bsq_kernels.hi
 # the same-byte-mix streaming kernel the bench compares the quantizers with
 CEILING_LIB = os.path.join(HERE, "libbsq_ceiling.so")
 CEILING_SOURCES = [os.path.join(CSRC, "bsq_ceiling.hip")]
+# the serving operators
+SERVING_LIB = os.path.join(HERE, "libbsq_serving.so")
+SERVING_SOURCES = [os.path.join(CSRC, f) for f in ("bsq_serving_api.cpp", "bsq_kv.hip",
+                                                   "bsq_pages.hip", "bsq_moe.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -34,8 +38,10 @@ FLAGS = [
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    """Build libbsq.so, then libbsq_ceiling.so; returns the path of the first."""
+    """Build libbsq.so, libbsq_serving.so and libbsq_ceiling.so; returns the path of the
+    first."""
     _build_one(LIB, SOURCES, verbose, extra)
+    _build_one(SERVING_LIB, SERVING_SOURCES, verbose, extra)
     _build_one(CEILING_LIB, CEILING_SOURCES, verbose, extra)
     return LIB
 

@@ -1,0 +1,646 @@
+// bsq_kv.hip -- gfx950 kernels of the paged 8-bit key/value cache: writing
+// tokens into it, attention over it.  include/bsq_serving.h states the
+// layouts and the arithmetic.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "bsq_serving_internal.h"
+
+namespace bsq {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256, kWaves = 4;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+// Sequence s of a call: rows [lo, lo + n), L tokens in all.  n = 0 when its
+// offsets or its length make no sense.
+struct Seq {
+    int64_t lo;
+    int32_t n, L;
+};
+__device__ __forceinline__ Seq load_seq(const KvSeqs& q, int s) {
+    const int64_t lo = q.row_offsets[s], hi = q.row_offsets[s + 1];
+    const int32_t L = q.kv_lens[s];
+    Seq r{lo, 0, L};
+    if (lo < hi && hi <= q.num_rows && hi - lo <= 0x7FFFFFFF && L >= 0) r.n = (int32_t)(hi - lo);
+    return r;
+}
+
+// ------------------------------------------------------------ append
+//
+// One workgroup per (page touched, head, K or V).  It reads its new tokens
+// once (at most 64 x 256 elements, held in registers), takes their largest
+// magnitude, and writes their codes; the codes already in the page are read
+// only when the scale grew.  Work items are 4 tokens x 4 elements: the four
+// tokens 4 m .. 4 m + 3 of one element are one dword of V, and four elements
+// of one token one dword of K, so the same item serves both layouts and
+// every store but those of a partial group of tokens is a dword.
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a) {
+    constexpr int kPieces = D / 4;                 // 4-element pieces of a token
+    constexpr int kItems = 16 * kPieces / kThreads;  // items of a thread in a full page
+    const int s = (int)(blockIdx.x / (uint32_t)a.pages_per_seq);
+    const int pi = (int)(blockIdx.x % (uint32_t)a.pages_per_seq);
+    const int head = (int)blockIdx.y, is_v = (int)blockIdx.z;
+    const Seq sq = load_seq(a.seqs, s);
+    const int64_t old = (int64_t)sq.L - sq.n;      // tokens held before
+    if (sq.n == 0 || old < 0) return;
+    const int64_t page_i = old / kKvPage + pi;
+    const int64_t base = page_i * kKvPage;
+    if (base >= sq.L || page_i >= a.seqs.max_pages) return;
+    const int t0 = (int)(base < old ? old - base : 0);                   // first new token
+    const int t1 = (int)(sq.L - base < kKvPage ? sq.L - base : kKvPage);  // end of them
+    const int32_t page = a.seqs.table[(int64_t)s * a.seqs.table_stride + page_i];
+    if (page < 0 || page >= a.cache.num_pages) return;
+    uint8_t* codes = (is_v ? a.cache.v_codes : a.cache.k_codes) +
+                     (int64_t)page * a.cache.page_stride + (int64_t)head * D * kKvPage;
+    uint8_t* scale = (is_v ? a.cache.v_scales : a.cache.k_scales) +
+                     (int64_t)page * a.cache.scale_stride + head;
+    const uint32_t was = t0 > 0 ? *scale : 0u;
+    const int64_t ldx = a.ldx[is_v];
+    const uint16_t* x = a.x[is_v] + (sq.lo + (base - old)) * ldx + (int64_t)head * D;
+
+    // item w: tokens 4 (w / kPieces) .., elements 4 (w % kPieces) ..
+    u32x2 v[kItems][4];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int w = (int)threadIdx.x + k * kThreads;
+        const int tq = 4 * (w / kPieces), d = 4 * (w % kPieces);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = tq + e;
+            v[k][e] = (u32x2){0u, 0u};
+            if (t >= t0 && t < t1) v[k][e] = *reinterpret_cast<const u32x2*>(x + t * ldx + d);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t m = v[k][e][c] & 0x7FFF7FFFu;
+                amax = max(amax, max(m & 0xFFFFu, m >> 16));
+            }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off));
+    __shared__ uint32_t red[kWaves];
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
+    __syncthreads();
+    amax = max(max(red[0], red[1]), max(red[2], red[3]));
+
+    const bool nan = amax >= 0x7F80u || was == 255u;
+    uint32_t byte = (uint32_t)max((int)(amax >> 7) - 8, 0);
+    byte = nan ? 255u : max(byte, was);
+    // 2^X for the conversion: the instruction reads the exponent field alone
+    const float sc = __uint_as_float((nan ? 127u : byte) << 23);
+    // 448 * 2^X as a BF16 pattern: larger magnitudes saturate to it
+    const uint32_t cap = (byte << 7) + 0x460u;
+    const u16x2 cap2 = __builtin_bit_cast(u16x2, cap | (cap << 16));
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int w = (int)threadIdx.x + k * kThreads;
+        const int tq = 4 * (w / kPieces), d = 4 * (w % kPieces);
+        uint32_t c[4];                             // 4 codes of token tq + e
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bf16x2 p[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t word = v[k][e][h];
+                const u16x2 m = __builtin_elementwise_min(
+                    __builtin_bit_cast(u16x2, word & 0x7FFF7FFFu), cap2);
+                p[h] = __builtin_bit_cast(bf16x2, __builtin_bit_cast(uint32_t, m) |
+                                                      (word & 0x80008000u));
+            }
+            i16x2 r = {0, 0};
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, p[0], sc, false);
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, p[1], sc, true);
+            c[e] = nan ? 0u : __builtin_bit_cast(uint32_t, r);
+        }
+        if (!is_v) {
+            uint8_t* o = codes + (d / 16) * (16 * kKvPage) + d % 16;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (tq + e >= t0 && tq + e < t1)
+                    *reinterpret_cast<uint32_t*>(o + (tq + e) * 16) = c[e];
+        } else {
+            // tokens 16 j + 4 g + e at 16 g + 4 j + e
+            uint8_t* o = codes + d * kKvPage + 16 * (tq / 4 % 4) + 4 * (tq / 16);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {          // element d + b, tokens tq .. tq + 3
+                const uint32_t word = ((c[0] >> (8 * b)) & 0xFFu) |
+                                      (((c[1] >> (8 * b)) & 0xFFu) << 8) |
+                                      (((c[2] >> (8 * b)) & 0xFFu) << 16) |
+                                      (((c[3] >> (8 * b)) & 0xFFu) << 24);
+                if (tq >= t0 && tq + 4 <= t1) {
+                    *reinterpret_cast<uint32_t*>(o + b * kKvPage) = word;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (tq + e >= t0 && tq + e < t1)
+                            o[b * kKvPage + e] = (uint8_t)(word >> (8 * e));
+                }
+            }
+        }
+    }
+    // the tokens that were there, on the grown scale; each thread owns whole
+    // tokens of one element, apart from the bytes written above
+    if (t0 > 0 && byte != was) {
+        const float fac = nan ? 0.0f : __builtin_ldexpf(1.0f, (int)was - (int)byte);
+        for (int w = (int)threadIdx.x; w < t0 * D; w += kThreads) {
+            const int t = w / D, d = w % D;
+            uint8_t* o = is_v ? codes + d * kKvPage + 16 * (t / 4 % 4) + 4 * (t / 16) + t % 4
+                              : codes + (d / 16) * (16 * kKvPage) + t * 16 + d % 16;
+            const float f =
+                __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)*o, 1.0f, false)[0] * fac;
+            i16x2 r = {0, 0};
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, f, 0.0f, 1.0f, false);
+            *o = nan ? 0 : (uint8_t)__builtin_bit_cast(uint32_t, r);
+        }
+    }
+    // `was` was read by every thread before the barrier above
+    if (threadIdx.x == 0) *scale = (uint8_t)byte;
+}
+
+// ------------------------------------------------------------ attention
+//
+// The products run transposed, so that nothing moves between lanes:
+//   S^T (tokens x columns) = K Q^T    mfma_f32_16x16x32_bf16, four 16-token tiles a page
+//   O^T (head_dim x columns) += V^T P^T   mfma_f32_16x16x32_f16
+// A column is a (query row, head of the group) pair.  Lane l serves column
+// l % 16 and group g = l / 16; its scores are the tokens 16 j + 4 g + e
+// (j the tile, e the register), which are the 16 bytes of V that the lane
+// loads for an element: its weights are the B operand of the second product
+// as they stand.  K's 16-byte pieces hold 16 elements of a token: two steps
+// of the contraction, whose order q shares.
+
+// 8 E4M3 codes, exactly, as BF16 / FP16.
+__device__ __forceinline__ bf16x8 to_bf16(uint32_t a, uint32_t b) {
+    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    return (bf16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+__device__ __forceinline__ f16x8 to_f16(uint32_t a, uint32_t b) {
+    const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
+    const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+    const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+    const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+    return (f16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+__device__ __forceinline__ float group_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float group_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// The running state of 16 CB columns: m the largest score so far (in units
+// of log 2), l this lane's share of the sum of 2^(score - m + 15), acc the
+// lane's part of O^T in units of 2^unit.  The shift by 15 keeps weights down
+// to 2^-29 of the largest normal FP16 numbers; it cancels in acc / l.
+constexpr float kShift = 15.0f;
+template <int D, int CB>
+struct AttState {
+    f32x4 acc[CB][D / 16];
+    float m[CB], l[CB];
+    int unit;
+};
+
+template <int D, int CB>
+__device__ __forceinline__ void init_state(AttState<D, CB>& st) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+        st.m[c] = -INFINITY;
+        st.l[c] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.acc[c][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    st.unit = -1000;
+}
+
+// What a wave needs of its columns to mask: each lane's column sees tokens
+// [first, last].
+template <int CB>
+struct Columns {
+    int first[CB], last[CB];         // per lane
+    int all_from, all_to;            // tokens that every column of the wave sees
+};
+
+// One page: kb / vb are byte pointers of the page's head (already offset for the
+// lane: K piece g of token l % 16, V element l % 16 at 16 g).
+template <int D, int CB>
+__device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<CB>& cols,
+                                            const bf16x8 (&q)[CB][D / 32], const uint8_t* kb,
+                                            const uint8_t* vb, uint32_t ks, uint32_t vs, int base,
+                                            int L, float c0) {
+    constexpr int KI = D / 64, VI = D / 16;
+    const int g = (int)(threadIdx.x & 63) >> 4;
+    u32x4 kf[4][KI], vf[VI];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < KI; ++i)
+            kf[j][i] = *reinterpret_cast<const u32x4*>(kb + i * 4096 + j * 256);
+#pragma unroll
+    for (int i = 0; i < VI; ++i) vf[i] = *reinterpret_cast<const u32x4*>(vb + i * 1024);
+
+    // scores in units of log 2; a NaN scale of either makes NaN of what it meets
+    float c = c0 * __builtin_ldexpf(1.0f, (int)ks - 127);
+    if (ks == 255u || vs == 255u) c = NAN;
+    float p[CB][16];
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        f32x4 s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < KI; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        to_bf16(kf[j][i][2 * h], kf[j][i][2 * h + 1]), q[cb][2 * i + h], s[j], 0,
+                        0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[cb][4 * j + e] = s[j][e] * c;
+    }
+    if (base < cols.all_from || base + kKvPage - 1 > cols.all_to) {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int t = base + 16 * (k / 4) + 4 * g + k % 4;
+                if (t < cols.first[cb] || t > cols.last[cb]) p[cb][k] = -INFINITY;
+            }
+    }
+    if (base + kKvPage > L) {        // bytes past the sequence's end may hold anything
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int left = L - (base + 16 * j + 4 * g);   // of the dword's four tokens
+            const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u
+                                                              : (1u << (8 * left)) - 1u;
+#pragma unroll
+            for (int i = 0; i < VI; ++i) vf[i][j] &= keep;
+        }
+    }
+    // acc is kept in units of the page's V scale; a far smaller scale is met half way
+    const int vexp = vs == 255u ? 0 : (int)vs - 127;
+    const int unit = max(vexp, st.unit - 60);
+    const float step = __builtin_ldexpf(1.0f, max(st.unit - unit, -200));
+    f16x8 pf[CB][2];
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        float m = p[cb][0];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) m = fmaxf(m, p[cb][k]);
+        m = fmaxf(st.m[cb], group_max(m));
+        const float off = kShift - (m == -INFINITY ? 0.0f : m);
+        const float alpha = __builtin_amdgcn_exp2f(st.m[cb] + off - kShift);
+        st.m[cb] = m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            p[cb][k] = __builtin_amdgcn_exp2f(p[cb][k] + off);
+            sum += p[cb][k];
+        }
+        st.l[cb] = st.l[cb] * alpha + sum;
+        if (vexp < unit) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) p[cb][k] = __builtin_ldexpf(p[cb][k], vexp - unit);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) pf[cb][u][k] = (_Float16)p[cb][8 * u + k];
+        const float f = alpha * step;
+#pragma unroll
+        for (int i = 0; i < VI; ++i) st.acc[cb][i] *= f;
+    }
+    st.unit = unit;
+#pragma unroll
+    for (int i = 0; i < VI; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const f16x8 va = to_f16(vf[i][2 * u], vf[i][2 * u + 1]);
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+                st.acc[cb][i] =
+                    __builtin_amdgcn_mfma_f32_16x16x32_f16(va, pf[cb][u], st.acc[cb][i], 0, 0, 0);
+        }
+}
+
+// Column c of a sequence: its row (i), head of the group and the tokens it sees.
+struct Column {
+    int i, head, first, last;
+};
+__device__ __forceinline__ Column column(const AttendArgs& a, const Seq& sq, int c) {
+    Column r;
+    r.i = c / a.group;
+    r.head = c - r.i * a.group;
+    r.last = sq.L - sq.n + r.i;
+    r.first = a.window > 0 && r.last - a.window + 1 > 0 ? (int)(r.last - a.window + 1) : 0;
+    return r;
+}
+
+template <int D, int CB>
+__device__ __forceinline__ void load_q(const AttendArgs& a, const Seq& sq, int kvh, int c0, int cols,
+                                       bf16x8 (&q)[CB][D / 32], Columns<CB>& v) {
+    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        const int c = c0 + 16 * cb + r;
+        const Column k = column(a, sq, c < cols ? c : cols - 1);
+        v.first[cb] = k.first;
+        v.last[cb] = k.last;
+        const uint16_t* src = a.q + (sq.lo + k.i) * a.ldq + (int64_t)(kvh * a.group + k.head) * D;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                q[cb][2 * i + h] =
+                    *reinterpret_cast<const bf16x8*>(src + 64 * i + 16 * g + 8 * h);
+    }
+    const int ce = min(c0 + 16 * CB, cols) - 1;
+    v.all_to = column(a, sq, c0).last;
+    v.all_from = column(a, sq, ce).first;
+}
+
+// The tokens' pages [p0, p1) that columns [c0, ce] see.
+__device__ __forceinline__ void page_range(const AttendArgs& a, const Seq& sq, int c0, int ce,
+                                           int& p0, int& p1) {
+    const int first = column(a, sq, c0).first, last = column(a, sq, ce).last;
+    p0 = first / kKvPage;
+    p1 = last < 0 ? 0 : min(last / kKvPage + 1, a.seqs.max_pages);
+    if (p1 < p0) p1 = p0;
+}
+
+// The result of a column: O = acc 2^unit / l, or the partial sums of a split.
+template <int D>
+__device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq, int kvh, int c,
+                                             int cols, int split, const f32x4 (&o)[D / 16], float m,
+                                             float l) {
+    const int g = (int)(threadIdx.x & 63) >> 4;
+    if (c >= cols) return;
+    const Column k = column(a, sq, c);
+    const int64_t row = sq.lo + k.i;
+    const int head = kvh * a.group + k.head;
+    if (a.splits > 1) {
+        const int64_t at = ((int64_t)split * a.seqs.num_rows + row) * a.num_q_heads + head;
+        float* dst = a.part_o + at * D;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i + 4 * g) = o[i];
+        if (g == 0) {
+            a.part_ml[2 * at] = m;
+            a.part_ml[2 * at + 1] = l;
+        }
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* dst = a.out + row * a.ldo + (int64_t)head * D;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        const bf16x2 x = {(__bf16)(o[i][0] * inv), (__bf16)(o[i][1] * inv)};
+        const bf16x2 y = {(__bf16)(o[i][2] * inv), (__bf16)(o[i][3] * inv)};
+        *reinterpret_cast<u32x2*>(dst + 16 * i + 4 * g) =
+            (u32x2){__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
+    }
+    if (a.lse && g == 0)
+        a.lse[row * a.num_q_heads + head] =
+            l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Few columns (decode): a workgroup takes 16 columns of one (sequence, head)
+// and a share of their pages, its waves every fourth page; their states meet
+// in LDS at the end.
+template <int D>
+__global__ void __launch_bounds__(kThreads) attend_split_kernel(const AttendArgs a) {
+    __shared__ float sm[kWaves][16], sl[kWaves][16];
+    __shared__ f32x4 so[2][D / 16][64];
+    uint32_t b = blockIdx.x;
+    const int split = (int)(b % (uint32_t)a.splits);
+    b /= (uint32_t)a.splits;
+    const int blk = (int)(b % (uint32_t)a.col_blocks);
+    b /= (uint32_t)a.col_blocks;
+    const int kvh = (int)(b % (uint32_t)a.cache.num_heads), s = (int)(b / (uint32_t)a.cache.num_heads);
+    const Seq sq = load_seq(a.seqs, s);
+    const int cols = (int)min((int64_t)sq.n * a.group, (int64_t)0x7FFFFFF0), c0 = 16 * blk;
+    if (c0 >= cols) return;
+    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    bf16x8 q[1][D / 32];
+    Columns<1> v;
+    load_q<D, 1>(a, sq, kvh, c0, cols, q, v);
+    int p0, p1;
+    page_range(a, sq, c0, min(c0 + 16, cols) - 1, p0, p1);
+    const int from = p0 + (int)((int64_t)(p1 - p0) * split / a.splits);
+    const int to = p0 + (int)((int64_t)(p1 - p0) * (split + 1) / a.splits);
+
+    AttState<D, 1> st;
+    init_state(st);
+    const float cc = a.scale * kLog2e;
+    const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
+    const int64_t head_off = (int64_t)kvh * D * kKvPage;
+    for (int p = from + wave; p < to; p += kWaves) {
+        const int32_t page = row[p];
+        if (page < 0 || page >= a.cache.num_pages) continue;
+        const uint8_t* kb = a.cache.k_codes + (int64_t)page * a.cache.page_stride + head_off;
+        const uint8_t* vb = a.cache.v_codes + (int64_t)page * a.cache.page_stride + head_off;
+        const int64_t so_ = (int64_t)page * a.cache.scale_stride + kvh;
+        attend_page<D, 1>(st, v, q, kb + g * 1024 + r * 16, vb + r * 64 + g * 16,
+                          a.cache.k_scales[so_], a.cache.v_scales[so_], p * kKvPage, sq.L, cc);
+    }
+    // one state from the waves' four: their largest m, sums scaled to it
+    const float l = group_sum(st.l[0]);
+    if (g == 0) {
+        sm[wave][r] = st.m[0];
+        sl[wave][r] = l;
+    }
+    __syncthreads();
+    const float m = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
+    const float ms = m == -INFINITY ? 0.0f : m;
+    const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(st.m[0] - ms - kShift),
+                                     max(st.unit, -200));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) st.acc[0][i] *= f;
+    if (wave >= 2) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) so[wave - 2][i][lane] = st.acc[0][i];
+    }
+    __syncthreads();
+    if (wave < 2) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.acc[0][i] += so[wave][i][lane];
+    }
+    __syncthreads();
+    if (wave == 1) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) so[0][i][lane] = st.acc[0][i];
+    }
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) st.acc[0][i] += so[0][i][lane];
+    float total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+        total += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - ms - kShift);
+    store_column<D>(a, sq, kvh, c0 + r, cols, split, st.acc[0], m, total);
+}
+
+// Many columns (a prompt): the waves of a workgroup take 16 CB columns each
+// and read the same pages.
+template <int D, int CB>
+__global__ void __launch_bounds__(kThreads) attend_rows_kernel(const AttendArgs a) {
+    uint32_t b = blockIdx.x;
+    const int blk = (int)(b % (uint32_t)a.col_blocks);
+    b /= (uint32_t)a.col_blocks;
+    const int kvh = (int)(b % (uint32_t)a.cache.num_heads), s = (int)(b / (uint32_t)a.cache.num_heads);
+    const Seq sq = load_seq(a.seqs, s);
+    const int cols = (int)min((int64_t)sq.n * a.group, (int64_t)0x7FFFFFF0);
+    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c0 = 16 * CB * (kWaves * blk + wave);
+    if (c0 >= cols) return;
+    bf16x8 q[CB][D / 32];
+    Columns<CB> v;
+    load_q<D, CB>(a, sq, kvh, c0, cols, q, v);
+    int p0, p1;
+    page_range(a, sq, c0, min(c0 + 16 * CB, cols) - 1, p0, p1);
+    AttState<D, CB> st;
+    init_state(st);
+    const float cc = a.scale * kLog2e;
+    const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
+    const int64_t head_off = (int64_t)kvh * D * kKvPage;
+    for (int p = p0; p < p1; ++p) {
+        const int32_t page = row[p];
+        if (page < 0 || page >= a.cache.num_pages) continue;
+        const uint8_t* kb = a.cache.k_codes + (int64_t)page * a.cache.page_stride + head_off;
+        const uint8_t* vb = a.cache.v_codes + (int64_t)page * a.cache.page_stride + head_off;
+        const int64_t so_ = (int64_t)page * a.cache.scale_stride + kvh;
+        attend_page<D, CB>(st, v, q, kb + g * 1024 + r * 16, vb + r * 64 + g * 16,
+                           a.cache.k_scales[so_], a.cache.v_scales[so_], p * kKvPage, sq.L, cc);
+    }
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        const float l = group_sum(st.l[cb]) * __builtin_ldexpf(1.0f, -(int)kShift);
+        const float f = __builtin_ldexpf(1.0f, max(st.unit - (int)kShift, -200));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.acc[cb][i] *= f;
+        store_column<D>(a, sq, kvh, c0 + 16 * cb + r, cols, 0, st.acc[cb], st.m[cb], l);
+    }
+}
+
+// Joins the splits' partial results: one wave per (row, head), a lane holding
+// D / 64 consecutive elements.
+template <int D>
+__global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a) {
+    constexpr int E = D / 64;
+    const int lane = (int)threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    const int head = (int)(w % a.num_q_heads);
+    const int64_t si = w / a.num_q_heads;
+    const int i = (int)(si % a.max_q);
+    const int64_t s = si / a.max_q;
+    if (s >= a.seqs.num_seqs) return;
+    const Seq sq = load_seq(a.seqs, (int)s);
+    if (i >= sq.n) return;
+    const int64_t row = sq.lo + i, at = row * a.num_q_heads + head;
+    const int64_t stride = a.seqs.num_rows * a.num_q_heads;
+    float m = -INFINITY;
+    for (int k = 0; k < a.splits; ++k) m = fmaxf(m, a.part_ml[2 * (at + k * stride)]);
+    const float ms = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int k = 0; k < a.splits; ++k) {
+        const int64_t p = at + k * stride;
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ms);
+        l += a.part_ml[2 * p + 1] * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += a.part_o[p * D + lane * E + e] * f;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __bf16* dst = reinterpret_cast<__bf16*>(a.out) + row * a.ldo + (int64_t)head * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[e] = (__bf16)(o[e] * inv);
+    if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <int D>
+void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+    const int64_t per = (int64_t)a.seqs.num_seqs * a.cache.num_heads * a.col_blocks;
+    if (p.rows_form) {
+        hipLaunchKernelGGL((attend_rows_kernel<D, D == 256 ? 1 : 2>), dim3((uint32_t)per),
+                           dim3(kThreads), 0, stream, a);
+        return;
+    }
+    hipLaunchKernelGGL((attend_split_kernel<D>), dim3((uint32_t)(per * a.splits)), dim3(kThreads),
+                       0, stream, a);
+    if (a.splits > 1) {
+        const int64_t pairs = (int64_t)a.seqs.num_seqs * a.max_q * a.num_q_heads;
+        hipLaunchKernelGGL((attend_join_kernel<D>), dim3((uint32_t)((pairs + kWaves - 1) / kWaves)),
+                           dim3(kThreads), 0, stream, a);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
+    const dim3 grid((uint32_t)((int64_t)a.seqs.num_seqs * a.pages_per_seq),
+                    (uint32_t)a.cache.num_heads, 2);
+    switch (a.cache.head_dim) {
+        case 64: hipLaunchKernelGGL(kv_append_kernel<64>, grid, dim3(kThreads), 0, stream, a); break;
+        case 128: hipLaunchKernelGGL(kv_append_kernel<128>, grid, dim3(kThreads), 0, stream, a); break;
+        default: hipLaunchKernelGGL(kv_append_kernel<256>, grid, dim3(kThreads), 0, stream, a); break;
+    }
+    return hipGetLastError();
+}
+
+AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
+                       int64_t max_q, int64_t max_kv, int64_t window) {
+    const int64_t cols = max_q * (num_q_heads / num_heads);
+    AttendPlan p;
+    p.rows_form = cols > 64;
+    const int64_t per_block = p.rows_form ? (head_dim == 256 ? 64 : 128) : 16;
+    p.col_blocks = (int32_t)((cols + per_block - 1) / per_block);
+    int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
+    if (window > 0 && window < max_kv) pages = (window + max_q) / kKvPage + 2;
+    // enough workgroups for three on each of the 256 CUs, with two pages at least for a wave
+    int64_t splits = 768 / (num_seqs * num_heads * p.col_blocks);
+    if (splits > pages / 8) splits = pages / 8;
+    if (splits > 256) splits = 256;
+    p.splits = p.rows_form || splits < 1 ? 1 : (int32_t)splits;
+    return p;
+}
+
+hipError_t launch_kv_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+    switch (a.cache.head_dim) {
+        case 64: attend<64>(a, p, stream); break;
+        case 128: attend<128>(a, p, stream); break;
+        default: attend<256>(a, p, stream); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace bsq
