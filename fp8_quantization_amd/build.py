@@ -25,6 +25,8 @@ CEILING_SOURCES = [os.path.join(CSRC, "bsq_ceiling.hip")]
 SERVING_LIB = os.path.join(HERE, "libbsq_serving.so")
 SERVING_SOURCES = [os.path.join(CSRC, f) for f in ("bsq_serving_api.cpp", "bsq_kv.hip",
                                                    "bsq_pages.hip", "bsq_moe.hip")]
+# their Python binding, a CPython extension over torch's C++ tensors
+SERVING_EXT = os.path.join(HERE, "_serving.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -42,19 +44,45 @@ def build(verbose: bool = False, extra=()) -> str:
     first."""
     _build_one(LIB, SOURCES, verbose, extra)
     _build_one(SERVING_LIB, SERVING_SOURCES, verbose, extra)
+    _build_ext(verbose)
     _build_one(CEILING_LIB, CEILING_SOURCES, verbose, extra)
     return LIB
 
 
 def _build_one(lib, sources, verbose, extra):
     tmp = lib + ".tmp"
-    cmd = [HIPCC, *FLAGS, *extra, *sources, "-o", tmp]
+    _compile(lib, [HIPCC, *FLAGS, *extra, *sources, "-o", tmp], tmp, verbose)
+
+
+def _build_ext(verbose):
+    """_serving.so: host C++ only, beside the library it links."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    include = os.path.join(base, "include")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = SERVING_EXT + ".tmp"
+    _compile(SERVING_EXT, [
+        "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
+        "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I" + os.path.join(ROOT, "include"), "-I" + include,
+        "-I" + os.path.join(include, "torch", "csrc", "api", "include"),
+        "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(rocm, "include"),
+        os.path.join(CSRC, "bsq_serving_py.cpp"), "-o", tmp, "-L" + HERE, "-l:libbsq_serving.so",
+        "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10",
+        "-lc10_hip", "-Wl,-rpath,$ORIGIN"], tmp, verbose)
+
+
+def _compile(lib, cmd, tmp, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed building {os.path.basename(lib)}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed building {os.path.basename(lib)}")
     noise = [ln for ln in (res.stdout + res.stderr).splitlines()
              if ln.strip() and "packed-fp32-ops" not in ln]
     if verbose and noise:

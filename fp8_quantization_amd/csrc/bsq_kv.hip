@@ -4,6 +4,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "bsq_serving_internal.h"
 
 namespace bsq {
@@ -453,16 +456,21 @@ __global__ void __launch_bounds__(kThreads) attend_split_kernel(const AttendArgs
     load_q<D, 1>(a, sq, kvh, c0, cols, q, v);
     int p0, p1;
     page_range(a, sq, c0, min(c0 + 16, cols) - 1, p0, p1);
-    const int from = p0 + (int)((int64_t)(p1 - p0) * split / a.splits);
-    const int to = p0 + (int)((int64_t)(p1 - p0) * (split + 1) / a.splits);
+    // runs of split_pages pages; the last split takes what is left, however many
+    const int64_t run = (int64_t)split * a.split_pages;
+    const int from = (int)min((int64_t)p1, p0 + run);
+    const int to = split + 1 == a.splits ? p1 : (int)min((int64_t)p1, p0 + run + a.split_pages);
+    if (split > 0 && from >= to) return;           // nor does the join look at it
 
     AttState<D, 1> st;
     init_state(st);
     const float cc = a.scale * kLog2e;
     const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
     const int64_t head_off = (int64_t)kvh * D * kKvPage;
+    int32_t next = from + wave < to ? row[from + wave] : 0;
     for (int p = from + wave; p < to; p += kWaves) {
-        const int32_t page = row[p];
+        const int32_t page = next;
+        next = p + kWaves < to ? row[p + kWaves] : 0;   // ahead of this page's loads
         if (page < 0 || page >= a.cache.num_pages) continue;
         const uint8_t* kb = a.cache.k_codes + (int64_t)page * a.cache.page_stride + head_off;
         const uint8_t* vb = a.cache.v_codes + (int64_t)page * a.cache.page_stride + head_off;
@@ -551,40 +559,55 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const AttendArgs 
     }
 }
 
-// Joins the splits' partial results: one wave per (row, head), a lane holding
-// D / 64 consecutive elements.
+// Joins the splits' partial results: a workgroup per (row, head).  Wave w takes
+// the splits w, w + 4, ..., a lane D / 64 consecutive elements; the waves' sums
+// are added in their order.
 template <int D>
 __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a) {
     constexpr int E = D / 64;
+    __shared__ float so[kWaves][D], sl[kWaves];
     const int lane = (int)threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    const int head = (int)(w % a.num_q_heads);
-    const int64_t si = w / a.num_q_heads;
-    const int i = (int)(si % a.max_q);
-    const int64_t s = si / a.max_q;
-    if (s >= a.seqs.num_seqs) return;
-    const Seq sq = load_seq(a.seqs, (int)s);
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int head = (int)(blockIdx.x % (uint32_t)a.num_q_heads);
+    const uint32_t si = blockIdx.x / (uint32_t)a.num_q_heads;
+    const int i = (int)(si % (uint32_t)a.max_q), s = (int)(si / (uint32_t)a.max_q);
+    const Seq sq = load_seq(a.seqs, s);
     if (i >= sq.n) return;
+    // splits past the sequence's pages hold nothing and are not read
+    const int c0 = (i * a.group + head % a.group) / 16 * 16;
+    int p0, p1;
+    page_range(a, sq, c0, (int)min((int64_t)c0 + 16, (int64_t)sq.n * a.group) - 1, p0, p1);
+    const int used = (int)min((int64_t)a.splits,
+                              ((int64_t)p1 - p0 + a.split_pages - 1) / a.split_pages);
     const int64_t row = sq.lo + i, at = row * a.num_q_heads + head;
     const int64_t stride = a.seqs.num_rows * a.num_q_heads;
     float m = -INFINITY;
-    for (int k = 0; k < a.splits; ++k) m = fmaxf(m, a.part_ml[2 * (at + k * stride)]);
+    for (int k = lane; k < used; k += 64) m = fmaxf(m, a.part_ml[2 * (at + k * stride)]);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
     const float ms = m == -INFINITY ? 0.0f : m;
     float l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int k = 0; k < a.splits; ++k) {
+#pragma unroll 4
+    for (int k = wave; k < used; k += kWaves) {
         const int64_t p = at + k * stride;
         const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ms);
         l += a.part_ml[2 * p + 1] * f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += a.part_o[p * D + lane * E + e] * f;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    __bf16* dst = reinterpret_cast<__bf16*>(a.out) + row * a.ldo + (int64_t)head * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) dst[e] = (__bf16)(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    for (int e = 0; e < E; ++e) so[wave][lane * E + e] = o[e];
+    if (lane == 0) sl[wave] = l;
+    __syncthreads();
+    l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __bf16* dst = reinterpret_cast<__bf16*>(a.out) + row * a.ldo + (int64_t)head * D;
+    for (int d = (int)threadIdx.x; d < D; d += kThreads)
+        dst[d] = (__bf16)(((so[0][d] + so[1][d]) + (so[2][d] + so[3][d])) * inv);
+    if (a.lse && threadIdx.x == 0)
+        a.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <int D>
@@ -599,8 +622,8 @@ void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
                        0, stream, a);
     if (a.splits > 1) {
         const int64_t pairs = (int64_t)a.seqs.num_seqs * a.max_q * a.num_q_heads;
-        hipLaunchKernelGGL((attend_join_kernel<D>), dim3((uint32_t)((pairs + kWaves - 1) / kWaves)),
-                           dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((attend_join_kernel<D>), dim3((uint32_t)pairs), dim3(kThreads), 0, stream,
+                           a);
     }
 }
 
@@ -617,6 +640,8 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16;
+
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window) {
     const int64_t cols = max_q * (num_q_heads / num_heads);
@@ -626,11 +651,15 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     p.col_blocks = (int32_t)((cols + per_block - 1) / per_block);
     int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
     if (window > 0 && window < max_kv) pages = (window + max_q) / kKvPage + 2;
-    // enough workgroups for three on each of the 256 CUs, with two pages at least for a wave
-    int64_t splits = 768 / (num_seqs * num_heads * p.col_blocks);
-    if (splits > pages / 8) splits = pages / 8;
-    if (splits > 256) splits = 256;
+    // runs of pages: kSplitTarget workgroups if every sequence were the longest, and
+    // kSplitLeast pages at least in a run
+    const double blocks = (double)num_seqs * (double)num_heads * p.col_blocks;
+    int64_t run = (int64_t)std::ceil(std::min((double)pages, (double)pages * blocks / kSplitTarget));
+    if (run < kSplitLeast) run = kSplitLeast;
+    run = (run + kWaves - 1) / kWaves * kWaves;
+    const int64_t splits = (pages + run - 1) / run;
     p.splits = p.rows_form || splits < 1 ? 1 : (int32_t)splits;
+    p.split_pages = (int32_t)run;
     return p;
 }
 

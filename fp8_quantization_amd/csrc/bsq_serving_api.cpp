@@ -262,6 +262,7 @@ int kv_cache_attention(const bsq_kv_cache* cache, const void* q, int64_t ldq, in
     a.max_q = (int32_t)max_q;
     a.col_blocks = p.col_blocks;
     a.splits = p.splits;
+    a.split_pages = p.split_pages;
     return launched(bsq::launch_kv_attend(a, p, static_cast<hipStream_t>(stream)));
 }
 
@@ -391,7 +392,7 @@ int64_t moe_few_tokens_workspace(int64_t num_tokens, int64_t inter, int64_t topk
         return -1;
     }
     ok();
-    return num_tokens * topk * inter * 2;
+    return num_tokens * topk * inter * 4;
 }
 
 int moe_few_tokens(int format, const void* x, int64_t ldx, int64_t num_tokens, int64_t hidden,

@@ -58,12 +58,14 @@ struct AttendArgs {
     int32_t max_q;
     int32_t col_blocks;              // workgroups over (row, head of the group) pairs
     int32_t splits;
+    int32_t split_pages;             // pages of a split
 };
 // How a call's work is cut; also what the workspace is sized by.
 struct AttendPlan {
     bool rows_form;                  // waves share the pages and split the columns (many rows)
     int32_t col_blocks;
     int32_t splits;
+    int32_t split_pages;
 };
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window);
@@ -114,7 +116,8 @@ struct MoeArgs {
     const float* logits;             // nullable
     int32_t* ids;
     float* weights;
-    uint16_t* h;                     // [num_tokens * topk][inter] BF16, workspace
+    uint16_t* h;                     // [num_tokens * topk][2][inter] BF16, workspace: h is the
+                                     // sum of the two
     uint16_t* y;
     int64_t ldy;
     int32_t tokens, hidden, inter, experts, topk;

@@ -239,7 +239,7 @@ int64_t kv_pages_compact_workspace(int64_t num_pages);
  *   y            BF16 [num_tokens][hidden], ldy as ldx.
  *   workspace    16-byte aligned, moe_few_tokens_workspace(...) bytes.
  * Products are summed in fp32, weights enter the matrix cores exactly (as
- * BF16), h times its weight is rounded to BF16 between the two products.
+ * BF16), and h as the sum of two BF16 numbers (16 bits).
  * The order of every sum is fixed.
  */
 int moe_few_tokens(int format, const void* x, int64_t ldx, int64_t num_tokens, int64_t hidden,
