@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "bsq_serving_internal.h"
 
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
 // as they stand.  K's 16-byte pieces hold 16 elements of a token: two steps
 // of the contraction, whose order q shares.
 
-// 8 E4M3 codes, exactly, as BF16 / FP16.
+// 8 E4M3 codes as BF16, and times a power of two as FP16.
 __device__ __forceinline__ bf16x8 to_bf16(uint32_t a, uint32_t b) {
     const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
     const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
@@ -198,32 +199,38 @@ __device__ __forceinline__ bf16x8 to_bf16(uint32_t a, uint32_t b) {
     const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
     return (bf16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
-__device__ __forceinline__ f16x8 to_f16(uint32_t a, uint32_t b) {
-    const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
-    const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
-    const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
-    const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+__device__ __forceinline__ f16x8 to_f16(uint32_t a, uint32_t b, float scale) {
+    const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, scale, false);
+    const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, scale, true);
+    const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, scale, false);
+    const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, scale, true);
     return (f16x8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
+// The largest, and the sum, over the four lanes that share a column.
 __device__ __forceinline__ float group_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+
 __device__ __forceinline__ float group_sum(float v) {
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
 }
 
-// The running state of 16 CB columns: m the largest score so far (in units
-// of log 2), l this lane's share of the sum of 2^(score - m + 15), acc the
-// lane's part of O^T in units of 2^unit.  The shift by 15 keeps weights down
-// to 2^-29 of the largest normal FP16 numbers; it cancels in acc / l.
-constexpr float kShift = 15.0f;
+// The running state of 16 CB columns.  Scores are in units of log 2; m is a
+// column's reference score, weights are 2^(score - m + kShift) and l and acc
+// (the lane's part of O^T, in units of 2^unit) their sums.  m follows the
+// largest score only when that passes it by kSlack: most pages then neither
+// rescale acc nor exchange their maxima between lanes.  Weights stay below
+// 2^(kShift + kSlack) = 2^15 and are normal FP16 numbers down to 2^-25 of m's.
+constexpr float kShift = 11.0f, kSlack = 4.0f;
 template <int D, int CB>
 struct AttState {
     f32x4 acc[CB][D / 16];
-    float m[CB], l[CB];
+    float m[CB], l[CB];              // l: the lane's share
     int unit;
 };
 
@@ -247,109 +254,134 @@ struct Columns {
     int all_from, all_to;            // tokens that every column of the wave sees
 };
 
-// One page: kb / vb are byte pointers of the page's head (already offset for the
-// lane: K piece g of token l % 16, V element l % 16 at 16 g).
-template <int D, int CB>
-__device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<CB>& cols,
-                                            const bf16x8 (&q)[CB][D / 32], const uint8_t* kb,
-                                            const uint8_t* vb, uint32_t ks, uint32_t vs, int base,
-                                            int L, float c0) {
-    constexpr int KI = D / 64, VI = D / 16;
-    const int g = (int)(threadIdx.x & 63) >> 4;
-    u32x4 kf[4][KI], vf[VI];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < KI; ++i)
-            kf[j][i] = *reinterpret_cast<const u32x4*>(kb + i * 4096 + j * 256);
-#pragma unroll
-    for (int i = 0; i < VI; ++i) vf[i] = *reinterpret_cast<const u32x4*>(vb + i * 1024);
+// V's scale goes into its conversion to FP16, relative to acc's unit: exact
+// within [-15, 7] of it.  Past that the unit moves, by 60 at most towards a
+// smaller scale (acc grows by as much).
+__device__ __forceinline__ int v_exponent(uint32_t vs) { return vs == 255u ? 0 : (int)vs - 127; }
+__device__ __forceinline__ int next_unit(int unit, uint32_t vs) {
+    const int e = v_exponent(vs);
+    return e > unit + 7 || e < unit - 15 ? max(e, unit - 60) : unit;
+}
+// 2^n for the n of units and scales; below the normal numbers 0.
+__device__ __forceinline__ float power_of_two(int n) {
+    return n < -126 ? 0.0f : __uint_as_float((uint32_t)(min(n, 127) + 127) << 23);
+}
+__device__ __forceinline__ float v_factor(uint32_t vs, int unit) {
+    return power_of_two(v_exponent(vs) - unit);
+}
+// Of the dword of V that holds tokens t .. t + 3, the bytes before the
+// sequence's end: those past it may hold anything.
+__device__ __forceinline__ uint32_t before_end(int t, int L) {
+    const int left = L - t;
+    return left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+}
 
-    // scores in units of log 2; a NaN scale of either makes NaN of what it meets
+template <int D, int CB>
+__device__ __forceinline__ void move_unit(AttState<D, CB>& st, int unit) {
+    const float step = power_of_two(st.unit - unit);
+    st.unit = unit;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.acc[cb][i] *= step;
+}
+
+// One page.  kf(j, k): the lane's 8 elements of K of token tile j and step k of
+// the contraction; vf(i, u): its 8 tokens of V of 16-element tile i and step u,
+// in units of 2^st.unit.
+template <int D, int CB, class KF, class VF>
+__device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<CB>& cols,
+                                            const bf16x8 (&q)[CB][D / 32], KF kf, VF vf, uint32_t ks,
+                                            uint32_t vs, int base, float c0) {
+    constexpr int VI = D / 16;
+    const int g = (int)(threadIdx.x & 63) >> 4;
+    f32x4 s[CB][4];
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[cb][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bf16x8 a = kf(j, k);
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+                s[cb][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[cb][k], s[cb][j], 0, 0, 0);
+        }
+    // to units of log 2; a NaN scale of K or V makes NaN of every weight it meets
     float c = c0 * __builtin_ldexpf(1.0f, (int)ks - 127);
     if (ks == 255u || vs == 255u) c = NAN;
-    float p[CB][16];
+    const bool masked = base < cols.all_from || base + kKvPage - 1 > cols.all_to;
+    // bit k: the column sees the lane's token k (16 (k / 4) + 4 g + k % 4)
+    uint32_t seen[CB];
+    float top[CB];
+    if (masked) {
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {
-        f32x4 s[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < KI; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        to_bf16(kf[j][i][2 * h], kf[j][i][2 * h + 1]), q[cb][2 * i + h], s[j], 0,
-                        0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[cb][4 * j + e] = s[j][e] * c;
-    }
-    if (base < cols.all_from || base + kKvPage - 1 > cols.all_to) {
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
+        for (int cb = 0; cb < CB; ++cb) {
+            seen[cb] = 0;
+            top[cb] = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const int t = base + 16 * (k / 4) + 4 * g + k % 4;
-                if (t < cols.first[cb] || t > cols.last[cb]) p[cb][k] = -INFINITY;
+                const bool in = t >= cols.first[cb] && t <= cols.last[cb];
+                seen[cb] |= in ? 1u << k : 0u;
+                top[cb] = fmaxf(top[cb], in ? s[cb][k / 4][k % 4] : -INFINITY);
             }
-    }
-    if (base + kKvPage > L) {        // bytes past the sequence's end may hold anything
+        }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int left = L - (base + 16 * j + 4 * g);   // of the dword's four tokens
-            const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u
-                                                              : (1u << (8 * left)) - 1u;
+        for (int cb = 0; cb < CB; ++cb) {
+            top[cb] = s[cb][0][0];
 #pragma unroll
-            for (int i = 0; i < VI; ++i) vf[i][j] &= keep;
+            for (int k = 1; k < 16; ++k) top[cb] = fmaxf(top[cb], s[cb][k / 4][k % 4]);
         }
     }
-    // acc is kept in units of the page's V scale; a far smaller scale is met half way
-    const int vexp = vs == 255u ? 0 : (int)vs - 127;
-    const int unit = max(vexp, st.unit - 60);
-    const float step = __builtin_ldexpf(1.0f, max(st.unit - unit, -200));
-    f16x8 pf[CB][2];
+    bool passed = false;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) passed |= top[cb] * c > st.m[cb] + kSlack;
+    if (__any(passed)) {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            // no score seen so far: alpha is 0 or, with none in this page either, 1
+            const float m = fmaxf(st.m[cb], group_max(top[cb]) * c);
+            const float alpha = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m[cb] - m);
+            st.m[cb] = m;
+            st.l[cb] *= alpha;
+#pragma unroll
+            for (int i = 0; i < VI; ++i) st.acc[cb][i] *= alpha;
+        }
+    }
+    f16x8 p[CB][2];
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
-        float m = p[cb][0];
+        const float off = kShift - (st.m[cb] == -INFINITY ? 0.0f : st.m[cb]);
+        float w[16];
 #pragma unroll
-        for (int k = 1; k < 16; ++k) m = fmaxf(m, p[cb][k]);
-        m = fmaxf(st.m[cb], group_max(m));
-        const float off = kShift - (m == -INFINITY ? 0.0f : m);
-        const float alpha = __builtin_amdgcn_exp2f(st.m[cb] + off - kShift);
-        st.m[cb] = m;
-        float sum = 0.0f;
+        for (int k = 0; k < 16; ++k)
+            w[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[cb][k / 4][k % 4], c, off));
+        if (masked) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            p[cb][k] = __builtin_amdgcn_exp2f(p[cb][k] + off);
-            sum += p[cb][k];
-        }
-        st.l[cb] = st.l[cb] * alpha + sum;
-        if (vexp < unit) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) p[cb][k] = __builtin_ldexpf(p[cb][k], vexp - unit);
+            for (int k = 0; k < 16; ++k)
+                if (!((seen[cb] >> k) & 1u)) w[k] = 0.0f;
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int k = 0; k < 16; ++k) p[cb][k / 8][k % 8] = (_Float16)w[k];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) pf[cb][u][k] = (_Float16)p[cb][8 * u + k];
-        const float f = alpha * step;
+        for (int n = 8; n >= 1; n /= 2)
 #pragma unroll
-        for (int i = 0; i < VI; ++i) st.acc[cb][i] *= f;
+            for (int k = 0; k < n; ++k) w[k] += w[k + n];
+        st.l[cb] += w[0];
     }
-    st.unit = unit;
 #pragma unroll
     for (int i = 0; i < VI; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const f16x8 va = to_f16(vf[i][2 * u], vf[i][2 * u + 1]);
+            const f16x8 a = vf(i, u);
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb)
                 st.acc[cb][i] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_f16(va, pf[cb][u], st.acc[cb][i], 0, 0, 0);
+                    __builtin_amdgcn_mfma_f32_16x16x32_f16(a, p[cb][u], st.acc[cb][i], 0, 0, 0);
         }
 }
 
@@ -370,6 +402,7 @@ template <int D, int CB>
 __device__ __forceinline__ void load_q(const AttendArgs& a, const Seq& sq, int kvh, int c0, int cols,
                                        bf16x8 (&q)[CB][D / 32], Columns<CB>& v) {
     const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;   // scores take |scale|
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
         const int c = c0 + 16 * cb + r;
@@ -381,8 +414,8 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const Seq& sq, int k
         for (int i = 0; i < D / 64; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                q[cb][2 * i + h] =
-                    *reinterpret_cast<const bf16x8*>(src + 64 * i + 16 * g + 8 * h);
+                q[cb][2 * i + h] = __builtin_bit_cast(
+                    bf16x8, *reinterpret_cast<const u32x4*>(src + 64 * i + 16 * g + 8 * h) ^ sign);
     }
     const int ce = min(c0 + 16 * CB, cols) - 1;
     v.all_to = column(a, sq, c0).last;
@@ -434,26 +467,26 @@ __device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq,
 }
 
 // Few columns (decode): a workgroup takes 16 columns of one (sequence, head)
-// and a share of their pages, its waves every fourth page; their states meet
-// in LDS at the end.
-template <int D>
-__global__ void __launch_bounds__(kThreads) attend_split_kernel(const AttendArgs a) {
-    __shared__ float sm[kWaves][16], sl[kWaves][16];
-    __shared__ f32x4 so[2][D / 16][64];
+// and a run of their pages, its W waves every W-th page; their states meet
+// in LDS at the end.  ONCE: no other workgroup reads these pages (one block of
+// columns), so they are loaded past the caches' retention.
+template <int D, int W, bool ONCE>
+__global__ void __launch_bounds__(64 * W, D == 256 ? 1 : W == 4 ? 3 : 2)
+attend_split_kernel(const AttendArgs a) {
+    __shared__ float sm[W][16], sl[W][16];
+    __shared__ f32x4 so[W / 2][D / 16][64];
+    // heads fastest: workgroups that run at the same time read the parts of a page
     uint32_t b = blockIdx.x;
-    const int split = (int)(b % (uint32_t)a.splits);
-    b /= (uint32_t)a.splits;
+    const int kvh = (int)(b % (uint32_t)a.cache.num_heads);
+    b /= (uint32_t)a.cache.num_heads;
     const int blk = (int)(b % (uint32_t)a.col_blocks);
     b /= (uint32_t)a.col_blocks;
-    const int kvh = (int)(b % (uint32_t)a.cache.num_heads), s = (int)(b / (uint32_t)a.cache.num_heads);
+    const int split = (int)(b % (uint32_t)a.splits), s = (int)(b / (uint32_t)a.splits);
     const Seq sq = load_seq(a.seqs, s);
     const int cols = (int)min((int64_t)sq.n * a.group, (int64_t)0x7FFFFFF0), c0 = 16 * blk;
     if (c0 >= cols) return;
     const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    bf16x8 q[1][D / 32];
-    Columns<1> v;
-    load_q<D, 1>(a, sq, kvh, c0, cols, q, v);
     int p0, p1;
     page_range(a, sq, c0, min(c0 + 16, cols) - 1, p0, p1);
     // runs of split_pages pages; the last split takes what is left, however many
@@ -461,94 +494,202 @@ __global__ void __launch_bounds__(kThreads) attend_split_kernel(const AttendArgs
     const int from = (int)min((int64_t)p1, p0 + run);
     const int to = split + 1 == a.splits ? p1 : (int)min((int64_t)p1, p0 + run + a.split_pages);
     if (split > 0 && from >= to) return;           // nor does the join look at it
+    const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
+    int32_t next = from + wave < to ? row[from + wave] : 0;
+    bf16x8 q[1][D / 32];
+    Columns<1> v;
+    load_q<D, 1>(a, sq, kvh, c0, cols, q, v);
 
     AttState<D, 1> st;
     init_state(st);
-    const float cc = a.scale * kLog2e;
-    const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
+    const float cc = __builtin_fabsf(a.scale) * kLog2e;
     const int64_t head_off = (int64_t)kvh * D * kKvPage;
-    int32_t next = from + wave < to ? row[from + wave] : 0;
-    for (int p = from + wave; p < to; p += kWaves) {
+    for (int p = from + wave; p < to; p += W) {
         const int32_t page = next;
-        next = p + kWaves < to ? row[p + kWaves] : 0;   // ahead of this page's loads
+        next = p + W < to ? row[p + W] : 0;        // ahead of this page's loads
         if (page < 0 || page >= a.cache.num_pages) continue;
-        const uint8_t* kb = a.cache.k_codes + (int64_t)page * a.cache.page_stride + head_off;
-        const uint8_t* vb = a.cache.v_codes + (int64_t)page * a.cache.page_stride + head_off;
+        const int64_t at = (int64_t)page * a.cache.page_stride + head_off;
+        const uint8_t* kb = a.cache.k_codes + at + g * 1024 + r * 16;
+        const uint8_t* vb = a.cache.v_codes + at + r * 64 + g * 16;
         const int64_t so_ = (int64_t)page * a.cache.scale_stride + kvh;
-        attend_page<D, 1>(st, v, q, kb + g * 1024 + r * 16, vb + r * 64 + g * 16,
-                          a.cache.k_scales[so_], a.cache.v_scales[so_], p * kKvPage, sq.L, cc);
+        auto load = [](const uint8_t* x) {
+            if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x));
+            else return *reinterpret_cast<const u32x4*>(x);
+        };
+        // all of the page's loads first
+        u32x4 kr[4][D / 64], vr[D / 16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) kr[j][i] = load(kb + i * 4096 + j * 256);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) vr[i] = load(vb + i * 1024);
+        const uint32_t ks = a.cache.k_scales[so_], vs = a.cache.v_scales[so_];
+        const int unit = next_unit(st.unit, vs);
+        if (unit != st.unit) move_unit(st, unit);
+        const float vf = v_factor(vs, unit);
+        if (p * kKvPage + kKvPage > sq.L) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    vr[i][j] &= before_end(p * kKvPage + 16 * j + 4 * g, sq.L);
+        }
+        attend_page<D, 1>(
+            st, v, q,
+            [&](int j, int k) {
+                const u32x4& x = kr[j][k / 2];
+                return to_bf16(x[2 * (k % 2)], x[2 * (k % 2) + 1]);
+            },
+            [&](int i, int u) { return to_f16(vr[i][2 * u], vr[i][2 * u + 1], vf); }, ks, vs,
+            p * kKvPage, cc);
     }
-    // one state from the waves' four: their largest m, sums scaled to it
+    // one state from the waves': their largest m, sums scaled to it
     const float l = group_sum(st.l[0]);
     if (g == 0) {
         sm[wave][r] = st.m[0];
         sl[wave][r] = l;
     }
     __syncthreads();
-    const float m = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
+    float m = sm[0][r];
+#pragma unroll
+    for (int w = 1; w < W; ++w) m = fmaxf(m, sm[w][r]);
     const float ms = m == -INFINITY ? 0.0f : m;
     const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(st.m[0] - ms - kShift),
                                      max(st.unit, -200));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) st.acc[0][i] *= f;
-    if (wave >= 2) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) so[wave - 2][i][lane] = st.acc[0][i];
-    }
-    __syncthreads();
-    if (wave < 2) {
+    for (int h = W / 2; h >= 1; h /= 2) {
+        if (wave >= h && wave < 2 * h) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) st.acc[0][i] += so[wave][i][lane];
-    }
-    __syncthreads();
-    if (wave == 1) {
+            for (int i = 0; i < D / 16; ++i) so[wave - h][i][lane] = st.acc[0][i];
+        }
+        __syncthreads();
+        if (wave < h) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) so[0][i][lane] = st.acc[0][i];
+            for (int i = 0; i < D / 16; ++i) st.acc[0][i] += so[wave][i][lane];
+        }
+        __syncthreads();
     }
-    __syncthreads();
     if (wave != 0) return;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) st.acc[0][i] += so[0][i][lane];
     float total = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
+    for (int w = 0; w < W; ++w)
         total += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - ms - kShift);
     store_column<D>(a, sq, kvh, c0 + r, cols, split, st.acc[0], m, total);
 }
 
 // Many columns (a prompt): the waves of a workgroup take 16 CB columns each
-// and read the same pages.
-template <int D, int CB>
-__global__ void __launch_bounds__(kThreads) attend_rows_kernel(const AttendArgs a) {
+// and read the same pages.  The workgroup converts a page once, K to BF16 and
+// V to FP16, into one of two LDS buffers while the other is used (the codes of
+// the page after it are on their way in registers): converted by every wave for
+// itself, the conversions were half of the vector instructions.  In LDS K is
+// [element / 8][token][8] and V [place / 8][element][8], the matrix
+// instruction's 16-byte operands, so 16 lanes read 256 consecutive bytes; V's
+// elements are kept at d ^ 4 (piece / 2), which spreads the 4 pieces that
+// 4 x 4 lanes write at once over the banks.
+template <int D, int CB, int W>
+__global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs a) {
+    constexpr int kHalf = D * kKvPage, kT = 64 * W, kLoads = kHalf / (kT * 16);
+    __shared__ bf16x8 k0[kHalf / 8], k1[kHalf / 8];
+    __shared__ f16x8 v0[kHalf / 8], v1[kHalf / 8];
     uint32_t b = blockIdx.x;
-    const int blk = (int)(b % (uint32_t)a.col_blocks);
-    b /= (uint32_t)a.col_blocks;
-    const int kvh = (int)(b % (uint32_t)a.cache.num_heads), s = (int)(b / (uint32_t)a.cache.num_heads);
+    const int kvh = (int)(b % (uint32_t)a.cache.num_heads);
+    b /= (uint32_t)a.cache.num_heads;
+    // the last rows, which see the most tokens, first
+    const int blk = a.col_blocks - 1 - (int)(b % (uint32_t)a.col_blocks);
+    const int s = (int)(b / (uint32_t)a.col_blocks);
     const Seq sq = load_seq(a.seqs, s);
     const int cols = (int)min((int64_t)sq.n * a.group, (int64_t)0x7FFFFFF0);
-    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int c0 = 16 * CB * (kWaves * blk + wave);
-    if (c0 >= cols) return;
+    const int tid = (int)threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w0 = 16 * CB * W * blk;              // the workgroup's first column
+    if (w0 >= cols) return;
+    const int c0 = w0 + 16 * CB * wave;
+    const bool mine = c0 < cols;
     bf16x8 q[CB][D / 32];
     Columns<CB> v;
-    load_q<D, CB>(a, sq, kvh, c0, cols, q, v);
-    int p0, p1;
-    page_range(a, sq, c0, min(c0 + 16 * CB, cols) - 1, p0, p1);
+    load_q<D, CB>(a, sq, kvh, mine ? c0 : w0, cols, q, v);
+    int p0, p1, q0 = 0, q1 = 0;                    // the workgroup's pages, the wave's
+    page_range(a, sq, w0, min(w0 + 16 * CB * W, cols) - 1, p0, p1);
+    if (mine) page_range(a, sq, c0, min(c0 + 16 * CB, cols) - 1, q0, q1);
     AttState<D, CB> st;
     init_state(st);
-    const float cc = a.scale * kLog2e;
+    const float cc = __builtin_fabsf(a.scale) * kLog2e;
     const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
     const int64_t head_off = (int64_t)kvh * D * kKvPage;
-    for (int p = p0; p < p1; ++p) {
+
+    // the codes of a page on their way: piece x = k kT + tid of K and of V, and its scales
+    // (a page outside the cache has K scale 256)
+    u32x4 kr[kLoads], vr[kLoads];
+    uint32_t ks_in = 256, vs_in = 0;
+    auto fetch = [&](int p) {
+        ks_in = 256;
+        if (p >= p1) return;
         const int32_t page = row[p];
-        if (page < 0 || page >= a.cache.num_pages) continue;
-        const uint8_t* kb = a.cache.k_codes + (int64_t)page * a.cache.page_stride + head_off;
-        const uint8_t* vb = a.cache.v_codes + (int64_t)page * a.cache.page_stride + head_off;
+        if (page < 0 || page >= a.cache.num_pages) return;
+        const int64_t at = (int64_t)page * a.cache.page_stride + head_off;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            kr[k] = *reinterpret_cast<const u32x4*>(a.cache.k_codes + at + (k * kT + tid) * 16);
+            vr[k] = *reinterpret_cast<const u32x4*>(a.cache.v_codes + at + (k * kT + tid) * 16);
+        }
         const int64_t so_ = (int64_t)page * a.cache.scale_stride + kvh;
-        attend_page<D, CB>(st, v, q, kb + g * 1024 + r * 16, vb + r * 64 + g * 16,
-                           a.cache.k_scales[so_], a.cache.v_scales[so_], p * kKvPage, sq.L, cc);
+        ks_in = a.cache.k_scales[so_];
+        vs_in = a.cache.v_scales[so_];
+    };
+    int unit_in = st.unit;                         // the unit of the page fetched last
+    auto convert = [&](int p, bf16x8* kb, f16x8* vb) {
+        if (ks_in == 256u) return;
+        unit_in = next_unit(unit_in, vs_in);
+        const float vf = v_factor(vs_in, unit_in);
+        if (p * kKvPage + kKvPage > sq.L) {
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    vr[k][j] &= before_end(p * kKvPage + 16 * j + 4 * (tid & 3), sq.L);
+        }
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int x = k * kT + tid;
+            bf16x8* ko = kb + (x >> 6) * 128 + (x & 63);      // 16-element chunk, token
+            ko[0] = to_bf16(kr[k][0], kr[k][1]);
+            ko[64] = to_bf16(kr[k][2], kr[k][3]);
+            const int y = x & 3, d = (x >> 2) ^ (4 * y);      // pieces 2 y and 2 y + 1
+            f16x8* vo = vb + 2 * y * D + d;
+            vo[0] = to_f16(vr[k][0], vr[k][1], vf);
+            vo[D] = to_f16(vr[k][2], vr[k][3], vf);
+        }
+    };
+    fetch(p0);
+    convert(p0, k0, v0);
+    uint32_t ks = ks_in, vs = vs_in;
+    int unit = unit_in;
+    fetch(p0 + 1);
+    auto page_step = [&](int p, const bf16x8* kb, const f16x8* vb, bf16x8* ko, f16x8* vo) {
+        // page p is in LDS, and no wave reads the other buffer any more
+        __syncthreads();
+        const uint32_t ks_now = ks, vs_now = vs;
+        const int unit_now = unit;
+        convert(p + 1, ko, vo);
+        ks = ks_in;
+        vs = vs_in;
+        unit = unit_in;
+        fetch(p + 2);
+        if (unit_now != st.unit) move_unit(st, unit_now);
+        if (p < q0 || p >= q1 || ks_now == 256u) return;
+        attend_page<D, CB>(
+            st, v, q, [&](int j, int k) { return kb[(8 * (k >> 1) + 2 * g + (k & 1)) * 64 + 16 * j + r]; },
+            [&](int i, int u) { return vb[(2 * g + u) * D + ((16 * i + r) ^ (4 * g))]; }, ks_now,
+            vs_now, p * kKvPage, cc);
+    };
+    for (int p = p0; p < p1; p += 2) {
+        page_step(p, k0, v0, k1, v1);
+        if (p + 1 < p1) page_step(p + 1, k1, v1, k0, v0);
     }
+    if (!mine) return;
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
         const float l = group_sum(st.l[cb]) * __builtin_ldexpf(1.0f, -(int)kShift);
@@ -610,16 +751,28 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
         a.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+// 16-column blocks of a wave and waves of a workgroup of the rows form (D = 256: one
+// block's sums fill the registers that two do at 128), 128 columns in all
+template <int D>
+constexpr int kRowBlocks = D == 256 ? 1 : 2;
+constexpr int kRowColumns = 128;
+
 template <int D>
 void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
     const int64_t per = (int64_t)a.seqs.num_seqs * a.cache.num_heads * a.col_blocks;
     if (p.rows_form) {
-        hipLaunchKernelGGL((attend_rows_kernel<D, D == 256 ? 1 : 2>), dim3((uint32_t)per),
-                           dim3(kThreads), 0, stream, a);
+        constexpr int W = kRowColumns / 16 / kRowBlocks<D>;
+        hipLaunchKernelGGL((attend_rows_kernel<D, kRowBlocks<D>, W>), dim3((uint32_t)per),
+                           dim3(64 * W), 0, stream, a);
         return;
     }
-    hipLaunchKernelGGL((attend_split_kernel<D>), dim3((uint32_t)(per * a.splits)), dim3(kThreads),
-                       0, stream, a);
+    const dim3 grid((uint32_t)(per * a.splits));
+    if (p.wide)
+        hipLaunchKernelGGL((attend_split_kernel<D, 8, false>), grid, dim3(512), 0, stream, a);
+    else if (a.col_blocks == 1)
+        hipLaunchKernelGGL((attend_split_kernel<D, 4, true>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attend_split_kernel<D, 4, false>), grid, dim3(256), 0, stream, a);
     if (a.splits > 1) {
         const int64_t pairs = (int64_t)a.seqs.num_seqs * a.max_q * a.num_q_heads;
         hipLaunchKernelGGL((attend_join_kernel<D>), dim3((uint32_t)pairs), dim3(kThreads), 0, stream,
@@ -647,7 +800,7 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     const int64_t cols = max_q * (num_q_heads / num_heads);
     AttendPlan p;
     p.rows_form = cols > 64;
-    const int64_t per_block = p.rows_form ? (head_dim == 256 ? 64 : 128) : 16;
+    const int64_t per_block = p.rows_form ? kRowColumns : 16;
     p.col_blocks = (int32_t)((cols + per_block - 1) / per_block);
     int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
     if (window > 0 && window < max_kv) pages = (window + max_q) / kKvPage + 2;
@@ -659,6 +812,8 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     run = (run + kWaves - 1) / kWaves * kWaves;
     const int64_t splits = (pages + run - 1) / run;
     p.splits = p.rows_form || splits < 1 ? 1 : (int32_t)splits;
+    // little work: eight waves share a run, so each walks half as many pages
+    p.wide = blocks * p.splits <= 256;
     p.split_pages = (int32_t)run;
     return p;
 }

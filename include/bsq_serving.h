@@ -116,9 +116,9 @@ int kv_cache_append(const bsq_kv_cache* cache, const void* k, int64_t ldk, const
  *
  * Scores, softmax statistics and sums are fp32; K and V codes enter the
  * matrix cores exactly (K as BF16 beside the BF16 queries, V as FP16), and
- * the softmax weights as FP16 scaled by 2^15 (11 bits down to 2^-29 of the
- * largest, an absolute 2^-40 below that).  The order of every sum is fixed:
- * equal inputs and sizes give equal bits.
+ * the softmax weights as FP16 numbers between 2^11 and 2^15 for the largest
+ * (11 bits down to 2^-25 of it, an absolute 2^-36 of it below that).  The
+ * order of every sum is fixed: equal inputs and sizes give equal bits.
  *
  *   q             BF16 [num_rows][num_q_heads][head_dim], ldq elements from a
  *                 row to the next (a multiple of 8), 16-byte aligned.
