@@ -374,9 +374,9 @@ __device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<C
         st.l[cb] += w[0];
     }
 #pragma unroll
-    for (int i = 0; i < VI; ++i)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int i = 0; i < VI; ++i) {
             const f16x8 a = vf(i, u);
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb)
@@ -586,9 +586,8 @@ attend_split_kernel(const AttendArgs a) {
 // the page after it are on their way in registers): converted by every wave for
 // itself, the conversions were half of the vector instructions.  In LDS K is
 // [element / 8][token][8] and V [place / 8][element][8], the matrix
-// instruction's 16-byte operands, so 16 lanes read 256 consecutive bytes; V's
-// elements are kept at d ^ 4 (piece / 2), which spreads the 4 pieces that
-// 4 x 4 lanes write at once over the banks.
+// instruction's 16-byte operands: 16 lanes read 256 consecutive bytes, and
+// write as many (each wave's 1 KiB of V is dealt to its lanes by columns).
 template <int D, int CB, int W>
 __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs a) {
     constexpr int kHalf = D * kKvPage, kT = 64 * W, kLoads = kHalf / (kT * 16);
@@ -620,36 +619,48 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
     const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
     const int64_t head_off = (int64_t)kvh * D * kKvPage;
 
-    // the codes of a page on their way: piece x = k kT + tid of K and of V, and its scales
-    // (a page outside the cache has K scale 256)
+    // Pages on their way, in registers: 16 pieces of 16 bytes a wave and load, and the scale
+    // bytes.  Page numbers are loaded one page ahead of that.  Both stay in vector
+    // registers until they are used (`lane0` hides that they are the same in all lanes):
+    // moved to scalar ones at the load, they made every page wait for its memory.
     u32x4 kr[kLoads], vr[kLoads];
-    uint32_t ks_in = 256, vs_in = 0;
+    uint32_t ks_v = 0, vs_v = 0;
+    int32_t page_v = -1;
+    int page_in = -1;                              // the page fetched last; -1: none
+    int lane0 = 0;
+    asm volatile("" : "+v"(lane0));
+    auto look_up = [&](int p) { page_v = row[min(p, p1 - 1) + lane0]; };
     auto fetch = [&](int p) {
-        ks_in = 256;
-        if (p >= p1) return;
-        const int32_t page = row[p];
-        if (page < 0 || page >= a.cache.num_pages) return;
-        const int64_t at = (int64_t)page * a.cache.page_stride + head_off;
+        const int page = __builtin_amdgcn_readfirstlane(page_v);
+        page_in = p < p1 && page >= 0 && page < a.cache.num_pages ? page : -1;
+        if (p + 1 < p1) look_up(p + 1);
+        if (page_in < 0) return;
+        const int64_t at = (int64_t)page_in * a.cache.page_stride + head_off;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
             kr[k] = *reinterpret_cast<const u32x4*>(a.cache.k_codes + at + (k * kT + tid) * 16);
-            vr[k] = *reinterpret_cast<const u32x4*>(a.cache.v_codes + at + (k * kT + tid) * 16);
+            vr[k] = *reinterpret_cast<const u32x4*>(a.cache.v_codes + at + (k * kT + (tid & ~63) + 4 * r + g) * 16);
         }
-        const int64_t so_ = (int64_t)page * a.cache.scale_stride + kvh;
-        ks_in = a.cache.k_scales[so_];
-        vs_in = a.cache.v_scales[so_];
+        const int64_t so_ = (int64_t)page_in * a.cache.scale_stride + kvh + lane0;
+        ks_v = a.cache.k_scales[so_];
+        vs_v = a.cache.v_scales[so_];
     };
-    int unit_in = st.unit;                         // the unit of the page fetched last
+    // scale bytes and unit of the page converted last (ks 256: it was none)
+    uint32_t ks = 256, vs = 0;
+    int unit = st.unit;
     auto convert = [&](int p, bf16x8* kb, f16x8* vb) {
-        if (ks_in == 256u) return;
-        unit_in = next_unit(unit_in, vs_in);
-        const float vf = v_factor(vs_in, unit_in);
+        ks = 256;
+        if (page_in < 0) return;
+        ks = __builtin_amdgcn_readfirstlane(ks_v);
+        vs = __builtin_amdgcn_readfirstlane(vs_v);
+        unit = next_unit(unit, vs);
+        const float vf = v_factor(vs, unit);
         if (p * kKvPage + kKvPage > sq.L) {
 #pragma unroll
             for (int k = 0; k < kLoads; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    vr[k][j] &= before_end(p * kKvPage + 16 * j + 4 * (tid & 3), sq.L);
+                    vr[k][j] &= before_end(p * kKvPage + 16 * j + 4 * g, sq.L);
         }
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
@@ -657,16 +668,14 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
             bf16x8* ko = kb + (x >> 6) * 128 + (x & 63);      // 16-element chunk, token
             ko[0] = to_bf16(kr[k][0], kr[k][1]);
             ko[64] = to_bf16(kr[k][2], kr[k][3]);
-            const int y = x & 3, d = (x >> 2) ^ (4 * y);      // pieces 2 y and 2 y + 1
-            f16x8* vo = vb + 2 * y * D + d;
+            f16x8* vo = vb + 2 * g * D + (x >> 6) * 16 + r;
             vo[0] = to_f16(vr[k][0], vr[k][1], vf);
             vo[D] = to_f16(vr[k][2], vr[k][3], vf);
         }
     };
+    if (p0 < p1) look_up(p0);
     fetch(p0);
     convert(p0, k0, v0);
-    uint32_t ks = ks_in, vs = vs_in;
-    int unit = unit_in;
     fetch(p0 + 1);
     auto page_step = [&](int p, const bf16x8* kb, const f16x8* vb, bf16x8* ko, f16x8* vo) {
         // page p is in LDS, and no wave reads the other buffer any more
@@ -674,15 +683,12 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
         const uint32_t ks_now = ks, vs_now = vs;
         const int unit_now = unit;
         convert(p + 1, ko, vo);
-        ks = ks_in;
-        vs = vs_in;
-        unit = unit_in;
         fetch(p + 2);
         if (unit_now != st.unit) move_unit(st, unit_now);
         if (p < q0 || p >= q1 || ks_now == 256u) return;
         attend_page<D, CB>(
             st, v, q, [&](int j, int k) { return kb[(8 * (k >> 1) + 2 * g + (k & 1)) * 64 + 16 * j + r]; },
-            [&](int i, int u) { return vb[(2 * g + u) * D + ((16 * i + r) ^ (4 * g))]; }, ks_now,
+            [&](int i, int u) { return vb[(2 * g + u) * D + (16 * i + r)]; }, ks_now,
             vs_now, p * kKvPage, cc);
     };
     for (int p = p0; p < p1; p += 2) {
