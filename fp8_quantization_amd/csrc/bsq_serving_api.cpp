@@ -384,15 +384,16 @@ int kv_pages_compact(const bsq_kv_cache* cache, const int32_t* block_table, int6
     return launched(bsq::launch_pages_compact(p, static_cast<hipStream_t>(stream)));
 }
 
-int64_t moe_few_tokens_workspace(int64_t num_tokens, int64_t inter, int64_t topk) {
+int64_t moe_few_tokens_workspace(int64_t num_tokens, int64_t hidden, int64_t inter, int64_t topk) {
     if (num_tokens < 0 || num_tokens > bsq::kMoeMaxTokens || topk < 1 || topk > bsq::kMoeMaxTopk ||
-        inter < 0 || inter > (int64_t(1) << 17) || inter % 128 != 0) {
-        fail(BSQ_ERR_INVALID_ARG, "num_tokens=%lld inter=%lld topk=%lld out of range",
-             (long long)num_tokens, (long long)inter, (long long)topk);
+        hidden < 0 || hidden > (int64_t(1) << 17) || hidden % 128 != 0 || inter < 0 ||
+        inter > (int64_t(1) << 17) || inter % 128 != 0) {
+        fail(BSQ_ERR_INVALID_ARG, "num_tokens=%lld hidden=%lld inter=%lld topk=%lld out of range",
+             (long long)num_tokens, (long long)hidden, (long long)inter, (long long)topk);
         return -1;
     }
     ok();
-    return num_tokens * topk * inter * 4;
+    return num_tokens * topk * 4 * (inter + (bsq::moe_is_few(num_tokens, topk) ? 0 : hidden));
 }
 
 int moe_few_tokens(int format, const void* x, int64_t ldx, int64_t num_tokens, int64_t hidden,
@@ -428,7 +429,7 @@ int moe_few_tokens(int format, const void* x, int64_t ldx, int64_t num_tokens, i
     if (!aligned(w13_codes, 16) || !aligned(w2_codes, 16) || !aligned(w13_scales, 4) ||
         !aligned(w2_scales, 4))
         return fail(BSQ_ERR_INVALID_ARG, "codes must be 16-byte and scales 4-byte aligned");
-    const int64_t need = moe_few_tokens_workspace(num_tokens, inter, topk);
+    const int64_t need = moe_few_tokens_workspace(num_tokens, hidden, inter, topk);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
         return fail(BSQ_ERR_INVALID_ARG,
                     "workspace (%p, %lld bytes) must be 16-byte aligned and hold %lld bytes",
@@ -446,6 +447,7 @@ int moe_few_tokens(int format, const void* x, int64_t ldx, int64_t num_tokens, i
     a.ids = topk_ids;
     a.weights = topk_weights;
     a.h = static_cast<uint16_t*>(workspace);
+    a.part = static_cast<float*>(workspace) + num_tokens * topk * inter;   // behind h
     a.y = static_cast<uint16_t*>(y);
     a.ldy = ldy;
     a.tokens = (int32_t)num_tokens;

@@ -119,12 +119,19 @@ struct MoeArgs {
     float* weights;
     uint16_t* h;                     // [num_tokens * topk][2][inter] BF16, workspace: h is the
                                      // sum of the two
+    float* part;                     // [num_tokens * topk][hidden], workspace of many entries
     uint16_t* y;
     int64_t ldy;
     int32_t tokens, hidden, inter, experts, topk;
     int32_t renormalize;
 };
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTopk = 16;
+// Entries (a token's choices of an expert) that one wave's lanes hold; few of them, for one
+// block of matrix columns, take the kernels without LDS tables and partial results.
+constexpr int kFewEntries = 64;
+inline bool moe_is_few(int64_t tokens, int64_t topk) {
+    return tokens <= 16 && tokens * topk <= kFewEntries;
+}
 hipError_t launch_moe(int fmt, const MoeArgs& a, hipStream_t stream);
 
 }  // namespace bsq

@@ -496,7 +496,7 @@ PyObject* moe(Args& a) {
     matrix(ids, "topk_ids", at::kInt, T, k);
     matrix(weights, "topk_weights", at::kFloat, T, k);
     // sizes that the workspace refuses are refused by the call, with its message
-    int64_t need = moe_few_tokens_workspace(T, I, k);
+    const int64_t need = moe_few_tokens_workspace(T, H, I, k);
     const Workspace ws(a, given, need < 0 ? 0 : need, stream);
     check(moe_few_tokens(fmt, x.data_ptr(), row_stride(x), T, H, I, E, k, w13->data_ptr(),
                          w13s->data_ptr(), w2->data_ptr(), w2s->data_ptr(),

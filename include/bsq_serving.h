@@ -203,9 +203,11 @@ int kv_pages_compact(const bsq_kv_cache* cache, const int32_t* block_table, int6
 int64_t kv_pages_compact_workspace(int64_t num_pages);
 
 /*
- * A mixture-of-experts layer for a few tokens, in two kernels: routing, gate
- * and up products with the SiLU gate, then the down products summed over
- * each token's experts.
+ * A mixture-of-experts layer for a few tokens.  With at most 16 tokens and 64
+ * (token, expert) entries it is two kernels: routing (of at most 4 tokens),
+ * gate and up products with the SiLU gate, then the down products summed over
+ * each token's experts.  More entries keep their parts of the down products
+ * apart, which a third kernel sums; more tokens are routed by one before.
  *
  *   y[t] = sum over the token's experts e of w_te * W2_e h_te   (BF16)
  *   h_te = silu(W1_e x_t) * (W3_e x_t)
@@ -250,7 +252,7 @@ int moe_few_tokens(int format, const void* x, int64_t ldx, int64_t num_tokens, i
                    int64_t workspace_bytes, void* stream);
 
 /* Bytes of moe_few_tokens' workspace, or -1 for sizes it would refuse. */
-int64_t moe_few_tokens_workspace(int64_t num_tokens, int64_t inter, int64_t topk);
+int64_t moe_few_tokens_workspace(int64_t num_tokens, int64_t hidden, int64_t inter, int64_t topk);
 
 /* Message of the calling thread's most recent failed call into this library
    ("" after a call that returned BSQ_OK). */
