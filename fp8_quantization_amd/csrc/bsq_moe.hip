@@ -27,71 +27,58 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-// A wave takes weights in steps of 128 bytes of each row, whole cache lines:
-// 256 elements of E2M1, 128 of E4M3, lane group g the 32 bytes at 32 g (64 or
-// 32 elements: two or one MX blocks).  A step is loaded while the one before it
-// is used.  (Lanes that took 16 bytes of each half line streamed at 4.4 TB/s
-// where these do at 6.)
+// A wave takes weights in steps of whole cache lines of each row: CH 128-element
+// chunks, 64 bytes of E2M1 codes or 128 of E4M3 each.  Of a chunk lane group g
+// takes the 32 elements at 32 g, one MX block; its scales in the step's chunks
+// are bytes of the dword that a BSQ_SCALES_MFMA16 record keeps for the lane.
 template <int FMT>
-constexpr int kStep = FMT == BSQ_MXFP8 ? 128 : 256;      // elements of a step
+constexpr int kLong = FMT == BSQ_MXFP8 ? 2 : 4;          // chunks in 256 bytes
 template <int FMT>
-constexpr int kHalves = kStep<FMT> / 128;                // MX blocks of a lane in a step
+constexpr int kShort = FMT == BSQ_MXFP8 ? 1 : 2;         // and in 128
+template <int FMT>
+constexpr int kLoads = FMT == BSQ_MXFP8 ? 2 : 1;         // 16-byte loads of a lane and chunk
 
-template <int NT>
+template <int FMT, int NT, int CH>
 struct Step {
-    u32x4 w[NT][2];
-    uint32_t s[NT][2];               // scale byte of each block
+    u32x4 w[NT][CH * kLoads<FMT>];
+    uint32_t s[NT];                  // scale bytes, chunk by chunk
 };
 
-// Where a lane's weights of NT 16-row tiles lie: its codes of step 0, and the scale of its
-// first block (the second's is 64 bytes on).
+// Where a lane's weights of NT 16-row tiles lie: its codes of chunk 0 and its dword of
+// record 0.
 template <int NT>
 struct Rows {
     const uint8_t* w[NT];
     const uint8_t* s[NT];
 };
-__device__ __forceinline__ int64_t group_bytes(int K) { return (int64_t)((K + 511) / 512) * 256; }
 
 // Rows row .. row + 15 (row a multiple of 16) of codes and scale records of K elements a row.
 template <int FMT, int NT>
 __device__ __forceinline__ void set_rows(Rows<NT>& p, int t, const uint8_t* codes,
                                          const uint8_t* scales, int64_t row, int K) {
     const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    p.w[t] = codes + (row + r) * (FMT == BSQ_MXFP8 ? K : K / 2) + 32 * g;
-    // block kb of a row has byte kb / 4 of dword row + 16 (kb % 4) in a record of 16 blocks
-    p.s[t] = scales + row / 16 * group_bytes(K) +
-             (FMT == BSQ_MXFP8 ? 4 * lane : 4 * (r + 16 * (2 * g & 3)) + (g >> 1));
+    p.w[t] = FMT == BSQ_MXFP8 ? codes + (row + r) * K + 32 * g : codes + (row + r) * (K / 2) + 16 * g;
+    p.s[t] = scales + row / 16 * ((int64_t)((K + 511) / 512) * 256) + 4 * lane;
 }
 
-// Step c.  An odd number of 128-element chunks leaves the last E2M1 step half full: its
-// lane groups 2 and 3 get zeros.
-template <int FMT, int NT>
-__device__ __forceinline__ Step<NT> load_step(const Rows<NT>& p, int c, int K) {
-    const bool out = FMT != BSQ_MXFP8 && (c + 1) * 256 > K && ((int)threadIdx.x & 32);
-    Step<NT> r;
+// Step c; chunks past the row's end repeat its last one.
+template <int FMT, int CH, int NT>
+__device__ __forceinline__ Step<FMT, NT, CH> load_step(const Rows<NT>& p, int c, int K) {
+    constexpr int L = kLoads<FMT>;
+    Step<FMT, NT, CH> r;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const u32x4* w = reinterpret_cast<const u32x4*>(p.w[t] + (int64_t)c * 128 - (out ? 64 : 0));
-        r.w[t][0] = __builtin_nontemporal_load(w);
-        r.w[t][1] = __builtin_nontemporal_load(w + 1);
-        if constexpr (FMT == BSQ_MXFP8) {
-            r.s[t][0] = p.s[t][(c >> 2) * 256 + (c & 3)];
-        } else {
-            const uint8_t* s = p.s[t] + (c >> 1) * 256 + 2 * (c & 1);
-            r.s[t][0] = s[0];
-            r.s[t][1] = s[64];
-        }
-    }
-    if constexpr (FMT != BSQ_MXFP8) {
-        if ((c + 1) * 256 > K) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < CH; ++i) {
+            const u32x4* w = reinterpret_cast<const u32x4*>(
+                p.w[t] + (int64_t)min(c * CH + i, K / 128 - 1) * (64 * L));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    r.w[t][h] = out ? (u32x4){0, 0, 0, 0} : r.w[t][h];
-                    r.s[t][h] = out ? 127u : r.s[t][h];
-                }
+            for (int k = 0; k < L; ++k) r.w[t][L * i + k] = __builtin_nontemporal_load(w + k);
         }
+        const uint8_t* s = p.s[t] + (int64_t)(c * CH >> 2) * 256 + (c * CH & 3);
+        if constexpr (CH == 4) r.s[t] = *reinterpret_cast<const uint32_t*>(s);
+        else if constexpr (CH == 2) r.s[t] = *reinterpret_cast<const uint16_t*>(s);
+        else r.s[t] = *s;
     }
     return r;
 }
@@ -101,44 +88,29 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
 }
 
-// The lane's 32 codes of tile t and block h, times their scale, as BF16: exact (a code's few
+// The lane's 32 codes of tile t and chunk i, times their scale, as BF16: exact (a code's few
 // bits times a power of two) wherever the product is a normal number.
-template <int FMT, int NT>
-__device__ __forceinline__ void convert(const Step<NT>& st, int t, int h, bf16x8 (&o)[4]) {
-    const float f = scale_of(st.s[t][h]);
+template <int FMT, int NT, int CH>
+__device__ __forceinline__ void convert(const Step<FMT, NT, CH>& st, int t, int i, bf16x8 (&o)[4]) {
+    const float f = scale_of((st.s[t] >> (8 * i)) & 255u);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         bf16x2 p[4];
         if constexpr (FMT == BSQ_MXFP8) {
-            const uint32_t a = st.w[t][s / 2][2 * (s % 2)], b = st.w[t][s / 2][2 * (s % 2) + 1];
+            const u32x4& w = st.w[t][2 * i + s / 2];
+            const uint32_t a = w[2 * (s % 2)], b = w[2 * (s % 2) + 1];
             p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, f, false);
             p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, f, true);
             p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, f, false);
             p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, f, true);
         } else {
-            const uint32_t a = st.w[t][h][s];
+            const uint32_t a = st.w[t][i][s];
             p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, f, 0);
             p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, f, 1);
             p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, f, 2);
             p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, f, 3);
         }
         o[s] = (bf16x8){p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
-    }
-}
-
-// Steps [c_from, c_to) of a wave: use(step, c) with the next one's loads in flight.
-template <int FMT, int NT, class F>
-__device__ __forceinline__ void for_steps(const Rows<NT>& w, int c_from, int c_to, int K, F use) {
-    if (c_from >= c_to) return;
-    Step<NT> s0 = load_step<FMT>(w, c_from, K), s1;
-    for (int c = c_from;; c += 2) {
-        // past the last step its loads repeat it
-        s1 = load_step<FMT>(w, min(c + 1, c_to - 1), K);
-        use(s0, c);
-        if (c + 1 >= c_to) break;
-        s0 = load_step<FMT>(w, min(c + 2, c_to - 1), K);
-        use(s1, c + 1);
-        if (c + 2 >= c_to) break;
     }
 }
 
@@ -355,7 +327,7 @@ __device__ __forceinline__ int many_entries(const MoeArgs& a, ManyEntries& m, in
 constexpr int kUpWaves = 4, kUpThreads = 64 * kUpWaves;
 
 template <int FMT, int NB, int G, RowsFrom FROM>
-__global__ void __launch_bounds__(kUpThreads, 2) moe_up_kernel(const MoeArgs a, int tiles) {
+__global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int tiles) {
     __shared__ f32x4 part[kUpWaves][2 * G][64];
     const int tid = (int)threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -402,8 +374,8 @@ __global__ void __launch_bounds__(kUpThreads, 2) moe_up_kernel(const MoeArgs a, 
         if (n == 0) return;
     }
 
-    constexpr int E = kStep<FMT> / 4;              // elements of a lane in a step
-    const int steps = (a.hidden + kStep<FMT> - 1) / kStep<FMT>;
+    constexpr int CH = kLong<FMT>, S = 128 * CH;
+    const int steps = (a.hidden + S - 1) / S;
     const int c_from = steps * wave / kUpWaves, c_to = steps * (wave + 1) / kUpWaves;
     Rows<2 * G> w;                                 // W1's tiles, then W3's
 #pragma unroll
@@ -423,38 +395,35 @@ __global__ void __launch_bounds__(kUpThreads, 2) moe_up_kernel(const MoeArgs a, 
         f32x4 acc[NB][2 * G];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            xr[b] = a.x + (row[b] / a.topk) * a.ldx + E * g;
+            xr[b] = a.x + (row[b] / a.topk) * a.ldx + 32 * g;
 #pragma unroll
             for (int t = 0; t < 2 * G; ++t) acc[b][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
         }
-        for_steps<FMT>(w, c_from, c_to, a.hidden, [&](const Step<2 * G>& st, int c) {
-            // lanes past the end of a row (whose weights are 0) read what lies before it
-            const bool out = c * kStep<FMT> + E * g >= a.hidden;
-            const int at = c * kStep<FMT> - (out ? 128 : 0);
+        for (int c = c_from; c < c_to; ++c) {
+            const auto st = load_step<FMT, CH>(w, c, a.hidden);
 #pragma unroll
-            for (int h = 0; h < kHalves<FMT>; ++h) {
-                bf16x8 ws[2 * G][4];
+            for (int i = 0; i < CH; ++i) {
+                const int at = c * S + 128 * i;
+                if (at >= a.hidden) break;
+                bf16x8 xs[NB][4];
 #pragma unroll
-                for (int t = 0; t < 2 * G; ++t) convert<FMT>(st, t, h, ws[t]);
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if (b > 0 && b0 + 16 * b >= n) break;
-                    bf16x8 xs[4];
+                    for (int s = 0; s < 4; ++s)
+                        xs[b][s] = *reinterpret_cast<const bf16x8*>(xr[b] + at + 8 * s);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        xs[s] = *reinterpret_cast<const bf16x8*>(xr[b] + at + 32 * h + 8 * s);
-                        if constexpr (FMT != BSQ_MXFP8)
-                            if ((c + 1) * 256 > a.hidden && out) xs[s] = (bf16x8){};
-                    }
+                for (int t = 0; t < 2 * G; ++t) {
+                    bf16x8 ws[4];
+                    convert<FMT>(st, t, i, ws);
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
 #pragma unroll
-                        for (int t = 0; t < 2 * G; ++t)
-                            acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[t][s], xs[s],
+                        for (int b = 0; b < NB; ++b)
+                            acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[s], xs[b][s],
                                                                                 acc[b][t], 0, 0, 0);
                 }
             }
-        });
+        }
         // the waves' sums in their order; lane l holds columns 4 g .. 4 g + 3 of row l % 16
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -501,7 +470,7 @@ constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
 
 template <int FMT>
 __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArgs a) {
-    constexpr int E = kStep<FMT> / 4;
+    constexpr int CH = kLong<FMT>, S = 128 * CH;
     __shared__ float sums[kDownWaves][16 * 16];    // [token][column]
     const int tid = (int)threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -515,7 +484,7 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
         firsts |= 1ull << at;
         m &= ~entries_of(few, expert_at(few, at));
     }
-    const int act = __popcll(firsts), steps = (a.inter + kStep<FMT> - 1) / kStep<FMT>;
+    const int act = __popcll(firsts), steps = (a.inter + S - 1) / S;
     const int col0 = 16 * (int)blockIdx.x;
     const int items = act * steps;
     const int it_from = items * wave / kDownWaves, it_to = items * (wave + 1) / kDownWaves;
@@ -528,27 +497,26 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
         const int ai = it / steps;
         Rows<1> w;
         set_rows<FMT>(w, 0, a.w2, a.w2_scales, (int64_t)expert_in_use(ai) * a.hidden + col0, a.inter);
-        return load_step<FMT>(w, it - ai * steps, a.inter);
+        return load_step<FMT, CH>(w, it - ai * steps, a.inter);
     };
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto use = [&](const Step<1>& st, int it) {
+    auto use = [&](const Step<FMT, 1, CH>& st, int it) {
         const int ai = it / steps, c = it - ai * steps;
         const uint64_t m = entries_of(few, expert_in_use(ai));
         int row[1];
         columns_of<1>(m, 0, row);
-        const bool out = c * kStep<FMT> + E * g >= a.inter;
-        const uint16_t* h0 = a.h + (int64_t)row[0] * 2 * a.inter + c * kStep<FMT> + E * g - (out ? 128 : 0);
+        const uint16_t* h0 = a.h + (int64_t)row[0] * 2 * a.inter + 32 * g;
 #pragma unroll
-        for (int h = 0; h < kHalves<FMT>; ++h) {
+        for (int i = 0; i < CH; ++i) {
+            const int at = c * S + 128 * i;
+            if (at >= a.inter) break;
             bf16x8 ws[4], hi[4], lo[4];
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                hi[s] = *reinterpret_cast<const bf16x8*>(h0 + 32 * h + 8 * s);
-                lo[s] = *reinterpret_cast<const bf16x8*>(h0 + a.inter + 32 * h + 8 * s);
-                if constexpr (FMT != BSQ_MXFP8)
-                    if ((c + 1) * 256 > a.inter && out) hi[s] = lo[s] = (bf16x8){};
+                hi[s] = *reinterpret_cast<const bf16x8*>(h0 + at + 8 * s);
+                lo[s] = *reinterpret_cast<const bf16x8*>(h0 + a.inter + at + 8 * s);
             }
-            convert<FMT>(st, 0, h, ws);
+            convert<FMT>(st, 0, i, ws);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[s], hi[s], acc, 0, 0, 0);
@@ -565,7 +533,7 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
         acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     };
     if (it_from < it_to) {
-        Step<1> s0 = load(it_from), s1;
+        Step<FMT, 1, CH> s0 = load(it_from), s1;
         for (int it = it_from;; it += 2) {
             // past the wave's last item its loads repeat that item's
             s1 = load(min(it + 1, it_to - 1));
@@ -587,94 +555,210 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
 
 // ------------------------------------------------------------ down, many entries
 //
-// A workgroup computes 256 columns of one expert's part, 32 a wave, for 16
-// entries at a time, whose h the waves share: it lies in LDS, 512 elements at a
-// time (read from memory by each wave for its 32 columns it was four times the
-// weights' loads, and half of the kernel's time).  The parts, times the
-// tokens' weights, go to memory in 32 bits, one row an entry, and a third
-// kernel adds a token's rows in their order.
+// A workgroup takes 256 columns, 32 a wave, and every splits-th expert in use.
+// Its work is a sequence of stages: 512 elements of the contraction for 16
+// entries of an expert, whose h the waves share in LDS (read from memory by each
+// wave for its 32 columns it was four times the weights' loads).  While a stage
+// is computed, the next one's h and the next steps' weights are on their way,
+// over the ends of experts too: a workgroup for each expert spent its life
+// waiting for its first loads (92 us, this form XX, of which the weights at
+// 6 TB/s are 33).  The parts, times the tokens' weights, go to memory in 32
+// bits, a row an entry, and a third kernel adds a token's rows in their order.
 
 constexpr int kStage = 512;          // elements of h in LDS
-// 16 bytes apart from a multiple of the banks' 256: 16 rows' pieces fall in different banks
+// 16 bytes more than a multiple of the banks' 256: 16 rows' pieces fall in different banks
 constexpr int kStageRow = kStage + 8;
 constexpr int kPartCols = 32 * kDownWaves;
 
-template <int FMT, RowsFrom FROM>
-__global__ void __launch_bounds__(kDownThreads, 2) moe_down_part_kernel(const MoeArgs a, int tiles) {
-    constexpr int E = kStep<FMT> / 4, kSteps = kStage / kStep<FMT>;
-    __shared__ ManyEntries many;
-    __shared__ __attribute__((aligned(16))) uint16_t stage[2][16][kStageRow];
+template <int FMT>
+__global__ void __launch_bounds__(kDownThreads, 4) moe_down_part_kernel(const MoeArgs a, int tiles,
+                                                                        int splits) {
+    constexpr int CH = kShort<FMT>, S = 128 * CH, kSteps = kStage / S;
+    constexpr int kEntries = kMoeMaxTokens * kMoeMaxTopk;
+    constexpr int kPieces = 16 * 2 * kStage / 8 / kDownThreads;   // 16-byte pieces of h a thread
+    __shared__ __attribute__((aligned(16))) uint16_t stage0[2 * 16 * kStageRow];
+    __shared__ __attribute__((aligned(16))) uint16_t stage1[2 * 16 * kStageRow];
+    __shared__ int16_t ids[kEntries];
+    __shared__ uint16_t order[kEntries];           // entries that count, by expert
+    __shared__ int count[kMoeMaxExperts];
+    __shared__ uint16_t first[kMoeMaxExperts];     // an expert's first place in `order`
+    __shared__ uint16_t active[kMoeMaxExperts + 1];// the experts in use, ascending
+    __shared__ int n_active, n_entries;
     const int tid = (int)threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int unit = (int)(blockIdx.x / (uint32_t)tiles), tile = (int)(blockIdx.x % (uint32_t)tiles);
-    int expert;
-    const int n = many_entries<FROM, kDownThreads>(a, many, unit, expert);
-    if (n == 0) return;
+    const int tile = (int)(blockIdx.x % (uint32_t)tiles), split = (int)(blockIdx.x / (uint32_t)tiles);
+    const int entries = a.tokens * a.topk;
+    for (int e = tid; e < a.experts; e += kDownThreads) count[e] = 0;
+    for (int r = tid; r < entries; r += kDownThreads) {
+        const int id = a.ids[r];
+        ids[r] = (int16_t)(id < 0 || id >= a.experts || a.weights[r] == 0.0f ? -1 : id);
+    }
+    __syncthreads();
+    for (int r = tid; r < entries; r += kDownThreads)
+        if (counts(ids, r, a.topk)) atomicAdd(&count[ids[r]], 1);
+    __syncthreads();
+    // the experts in use and where their entries start, by the first wave
+    if (wave == 0) {
+        int base = 0, used_experts = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const int e = e0 + lane, c = e < a.experts ? count[e] : 0;
+            int x = c;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int y = __shfl_up(x, off);
+                if (lane >= off) x += y;
+            }
+            const uint64_t used = __ballot(c > 0);
+            if (e < a.experts) first[e] = (uint16_t)(base + x - c);
+            if (c > 0) active[used_experts + __popcll(used & ((1ull << lane) - 1))] = (uint16_t)e;
+            used_experts += __popcll(used);
+            base += __shfl(x, 63);
+        }
+        if (lane == 0) {
+            n_active = used_experts;
+            n_entries = base;
+        }
+    }
+    __syncthreads();
+    // an expert's entries in any order: each is a column of its own
+    for (int r = tid; r < entries; r += kDownThreads)
+        if (counts(ids, r, a.topk)) {
+            const int id = ids[r];
+            order[first[id] + atomicSub(&count[id], 1) - 1] = (uint16_t)r;
+        }
+    __syncthreads();
+    const int act = n_active;
+    if (split >= act) return;
+
     const int col0 = kPartCols * tile + 32 * wave;
     const bool mine = col0 < a.hidden;             // hidden is a multiple of 128
-    const int steps = (a.inter + kStep<FMT> - 1) / kStep<FMT>;
-    Rows<2> w;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-        set_rows<FMT>(w, t, a.w2, a.w2_scales,
-                      (int64_t)expert * a.hidden + (mine ? col0 : 0) + 16 * t, a.inter);
-    for (int b0 = 0; b0 < n; b0 += 16) {
-        const int rows = min(16, n - b0), r = min(r16, rows - 1);
-        f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-        Step<2> s0 = load_step<FMT>(w, 0, a.inter), s1;
-        auto use = [&](const Step<2>& st, int c) {
-            const uint16_t* h0 = &stage[0][r][c % kSteps * kStep<FMT> + E * g];
-#pragma unroll
-            for (int h = 0; h < kHalves<FMT>; ++h) {
-                bf16x8 ws[2][4];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) convert<FMT>(st, t, h, ws[t]);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const bf16x8 hi = *reinterpret_cast<const bf16x8*>(h0 + 32 * h + 8 * s);
-                    const bf16x8 lo =
-                        *reinterpret_cast<const bf16x8*>(h0 + 16 * kStageRow + 32 * h + 8 * s);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[t][s], hi, acc[t], 0, 0, 0);
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[t][s], lo, acc[t], 0, 0, 0);
-                    }
-                }
-            }
-        };
-        for (int c0 = 0; c0 < steps; c0 += kSteps) {
-            // the entries' next 512 elements of both numbers of h, zeros past the end
-            __syncthreads();
-            for (int k = tid; k < rows * 2 * (kStage / 8); k += kDownThreads) {
-                const int piece = k % (kStage / 8), half = k / (kStage / 8) & 1, row = k / (kStage / 4);
-                const int at = c0 * kStep<FMT> + 8 * piece;
-                u32x4 v = {0, 0, 0, 0};
-                if (at < a.inter)
-                    v = *reinterpret_cast<const u32x4*>(
-                        a.h + ((int64_t)many.rows[b0 + row] * 2 + half) * a.inter + at);
-                *reinterpret_cast<u32x4*>(&stage[half][row][8 * piece]) = v;
-            }
-            __syncthreads();
-            // two steps at a time, the next one's loads in flight
-#pragma unroll
-            for (int k = 0; k < kSteps; k += 2) {
-                const int c = c0 + k;
-                if (c >= steps) break;
-                s1 = load_step<FMT>(w, min(c + 1, steps - 1), a.inter);
-                use(s0, c);
-                if (c + 1 >= steps) break;
-                s0 = load_step<FMT>(w, min(c + 2, steps - 1), a.inter);
-                use(s1, c + 1);
-            }
-        }
-        if (!mine || r16 >= rows) continue;
-        const int e = many.rows[b0 + r16], t0 = e / a.topk * a.topk;
-        float f = 0.0f;                            // of the equal entries of the token
-        for (int k = t0; k < t0 + a.topk; ++k)
-            if (many.ids[k] == expert) f += a.weights[k];
+    const int steps = (a.inter + S - 1) / S;
+    // a place in the sequence of stages (and, for the weights, a step of the stage)
+    struct Place {
+        int ai, expert, begin, n, b0, c;           // entries order[begin ..]; b0 the first of 16
+    };
+    auto enter = [&](Place& p, int ai) {
+        p.ai = ai;
+        p.b0 = p.c = 0;
+        if (ai >= act) return;
+        p.expert = __builtin_amdgcn_readfirstlane((int)active[ai]);
+        p.begin = __builtin_amdgcn_readfirstlane((int)first[p.expert]);
+        p.n = (ai + 1 < act ? __builtin_amdgcn_readfirstlane((int)first[active[ai + 1]]) : n_entries) -
+              p.begin;
+    };
+    // to the step `by` further; past the last one ai >= act
+    auto advance = [&](Place& p, int by) {
+        p.c += by;
+        if (p.c < steps) return;
+        p.c = 0;
+        p.b0 += 16;
+        if (p.b0 >= p.n) enter(p, p.ai + splits);
+    };
+    auto load = [&](const Place& p) {
+        Rows<2> w;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            *reinterpret_cast<f32x4*>(a.part + (int64_t)e * a.hidden + col0 + 16 * t + 4 * g) = acc[t] * f;
+            set_rows<FMT>(w, t, a.w2, a.w2_scales,
+                          (int64_t)p.expert * a.hidden + (mine ? col0 : 0) + 16 * t, a.inter);
+        return load_step<FMT, CH>(w, p.c, a.inter);
+    };
+    u32x4 hv[kPieces];
+    auto fetch = [&](const Place& p) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int x = k * kDownThreads + tid;
+            const int piece = x % (kStage / 8), half = x / (kStage / 8) & 1, row = x / (kStage / 4);
+            const int at = p.c * S + 8 * piece;
+            hv[k] = (u32x4){0, 0, 0, 0};
+            if (p.b0 + row < p.n && at < a.inter)
+                hv[k] = *reinterpret_cast<const u32x4*>(
+                    a.h + ((int64_t)order[p.begin + p.b0 + row] * 2 + half) * a.inter + at);
+        }
+    };
+    auto keep = [&](const Place& p, uint16_t* stage) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int x = k * kDownThreads + tid;
+            const int piece = x % (kStage / 8), half = x / (kStage / 8) & 1, row = x / (kStage / 4);
+            if (p.b0 + row < p.n)
+                *reinterpret_cast<u32x4*>(stage + (half * 16 + row) * kStageRow + 8 * piece) = hv[k];
+        }
+    };
+    f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    Place at, ahead, next;                         // this stage; the weights' step; the next stage
+    enter(at, split);
+    ahead = at;
+    Step<FMT, 2, CH> s0 = load(ahead), s1;
+    advance(ahead, 1);
+    fetch(at);
+    keep(at, stage0);
+    auto step = [&](const Step<FMT, 2, CH>& st, const uint16_t* h0) {
+        // chunks past the end meet zeros of h
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            bf16x8 ws[2][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) convert<FMT>(st, t, i, ws[t]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const bf16x8 hi = *reinterpret_cast<const bf16x8*>(h0 + 128 * i + 8 * s);
+                const bf16x8 lo = *reinterpret_cast<const bf16x8*>(h0 + 16 * kStageRow + 128 * i + 8 * s);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[t][s], hi, acc[t], 0, 0, 0);
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[t][s], lo, acc[t], 0, 0, 0);
+                }
+            }
+        }
+    };
+    auto one_stage = [&](const uint16_t* now, uint16_t* other) {
+        // this stage's h is in LDS, and no wave reads the other buffer any more
+        __syncthreads();
+        next = at;
+        advance(next, kSteps);
+        if (next.ai < act) fetch(next);
+        const int rows = min(16, at.n - at.b0), r = min(r16, rows - 1);
+        const uint16_t* h0 = now + r * kStageRow + 32 * g;
+        // s0 is the stage's first step, and the next stage's afterwards
+#pragma unroll
+        for (int k = 0; k < kSteps; k += 2) {
+            if (at.c + k >= steps) break;
+            if (ahead.ai < act) {
+                s1 = load(ahead);
+                advance(ahead, 1);
+            }
+            step(s0, h0 + k * S);
+            if (at.c + k + 1 >= steps) {
+                s0 = s1;
+                break;
+            }
+            if (ahead.ai < act) {
+                s0 = load(ahead);
+                advance(ahead, 1);
+            }
+            step(s1, h0 + (k + 1) * S);
+        }
+        if (at.c + kSteps >= steps) {              // the 16 entries' last stage
+            const int e = order[at.begin + at.b0 + r];
+            float f = 0.0f;                        // of the equal entries of the token
+            for (int k = e / a.topk * a.topk; k < (e / a.topk + 1) * a.topk; ++k)
+                if (ids[k] == at.expert) f += a.weights[k];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (mine && r16 < rows)
+                    *reinterpret_cast<f32x4*>(a.part + (int64_t)e * a.hidden + col0 + 16 * t + 4 * g) =
+                        acc[t] * f;
+                acc[t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            }
+        }
+        if (next.ai < act) keep(next, other);
+        at = next;
+    };
+    while (true) {
+        one_stage(stage0, stage1);
+        if (at.ai >= act) break;
+        one_stage(stage1, stage0);
+        if (at.ai >= act) break;
     }
 }
 
@@ -741,14 +825,11 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
                            dim3(kDownThreads), 0, stream, a);
         return hipGetLastError();
     }
+    // two workgroups for each of the 256 CUs, or one for each expert
     const int tiles = (a.hidden + kPartCols - 1) / kPartCols;
-    const dim3 grid((uint32_t)(units * tiles));
-    if (entries <= a.experts)
-        hipLaunchKernelGGL((moe_down_part_kernel<FMT, kEntry>), grid, dim3(kDownThreads), 0, stream, a,
-                           tiles);
-    else
-        hipLaunchKernelGGL((moe_down_part_kernel<FMT, kExpert>), grid, dim3(kDownThreads), 0, stream, a,
-                           tiles);
+    const int splits = std::max(1, std::min(units, 512 / tiles));
+    hipLaunchKernelGGL(moe_down_part_kernel<FMT>, dim3((uint32_t)(tiles * splits)), dim3(kDownThreads),
+                       0, stream, a, tiles, splits);
     hipLaunchKernelGGL(moe_sum_kernel, dim3((uint32_t)((a.hidden + 1023) / 1024), (uint32_t)a.tokens),
                        dim3(256), 0, stream, a);
     return hipGetLastError();
