@@ -43,20 +43,34 @@ __device__ __forceinline__ Seq load_seq(const KvSeqs& q, int s) {
 // ------------------------------------------------------------ append
 //
 // One workgroup per (page touched, head, K or V).  It reads its new tokens
-// once (at most 64 x 256 elements, held in registers), takes their largest
-// magnitude, and writes their codes; the codes already in the page are read
-// only when the scale grew.  Work items are 4 tokens x 4 elements: the four
-// tokens 4 m .. 4 m + 3 of one element are one dword of V, and four elements
-// of one token one dword of K, so the same item serves both layouts and
-// every store but those of a partial group of tokens is a dword.
+// once, held in registers, takes their largest magnitude, and writes their
+// codes; the codes already in the page are read only when the scale grew.
+// Work items are 4 tokens x 4 elements: the four tokens 4 m .. 4 m + 3 of one
+// element are one dword of V, and four elements of one token one dword of K,
+// so the same item serves both layouts and every store but those of a partial
+// group of tokens is a dword.  A page that is filled whole goes through LDS and
+// leaves in 16-byte stores (from the items' dwords, V's each in a line of its
+// own, 16384 tokens of 8 heads of 128 took XX us, this way YY).  A few tokens a
+// sequence (decode) take one wave and no barrier.
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a) {
+// Four E4M3 codes times a power of two, rounded to E4M3 again.
+__device__ __forceinline__ uint32_t rescale_codes(uint32_t v, float f) {
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v, 1.0f, false);
+    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v, 1.0f, true);
+    i16x2 r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a[0] * f, a[1] * f, 1.0f, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, b[0] * f, b[1] * f, 1.0f, true);
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// QUADS: groups of 4 tokens that a page's new tokens touch, at most
+template <int D, int THREADS, int QUADS>
+__global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs a) {
     constexpr int kPieces = D / 4;                 // 4-element pieces of a token
-    constexpr int kItems = 16 * kPieces / kThreads;  // items of a thread in a full page
+    constexpr int kItems = (QUADS * kPieces + THREADS - 1) / THREADS;
     const int s = (int)(blockIdx.x / (uint32_t)a.pages_per_seq);
     const int pi = (int)(blockIdx.x % (uint32_t)a.pages_per_seq);
-    const int head = (int)blockIdx.y, is_v = (int)blockIdx.z;
+    const int head = (int)blockIdx.y, is_v = (int)blockIdx.z, tid = (int)threadIdx.x;
     const Seq sq = load_seq(a.seqs, s);
     const int64_t old = (int64_t)sq.L - sq.n;      // tokens held before
     if (sq.n == 0 || old < 0) return;
@@ -66,22 +80,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
     const int t0 = (int)(base < old ? old - base : 0);                   // first new token
     const int t1 = (int)(sq.L - base < kKvPage ? sq.L - base : kKvPage);  // end of them
     const int32_t page = a.seqs.table[(int64_t)s * a.seqs.table_stride + page_i];
-    if (page < 0 || page >= a.cache.num_pages) return;
-    uint8_t* codes = (is_v ? a.cache.v_codes : a.cache.k_codes) +
-                     (int64_t)page * a.cache.page_stride + (int64_t)head * D * kKvPage;
-    uint8_t* scale = (is_v ? a.cache.v_scales : a.cache.k_scales) +
-                     (int64_t)page * a.cache.scale_stride + head;
-    const uint32_t was = t0 > 0 ? *scale : 0u;
     const int64_t ldx = a.ldx[is_v];
     const uint16_t* x = a.x[is_v] + (sq.lo + (base - old)) * ldx + (int64_t)head * D;
 
-    // item w: tokens 4 (w / kPieces) .., elements 4 (w % kPieces) ..
+    // item w: tokens 4 (t0 / 4 + w / kPieces) .., elements 4 (w % kPieces) ..
+    const int q0 = t0 / 4;
     u32x2 v[kItems][4];
-    uint32_t amax = 0;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-        const int w = (int)threadIdx.x + k * kThreads;
-        const int tq = 4 * (w / kPieces), d = 4 * (w % kPieces);
+        const int w = tid + k * THREADS;
+        const int tq = 4 * (q0 + w / kPieces), d = 4 * (w % kPieces);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int t = tq + e;
@@ -89,6 +97,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
             if (t >= t0 && t < t1) v[k][e] = *reinterpret_cast<const u32x2*>(x + t * ldx + d);
         }
     }
+    if (page < 0 || page >= a.cache.num_pages) return;
+    uint8_t* codes = (is_v ? a.cache.v_codes : a.cache.k_codes) +
+                     (int64_t)page * a.cache.page_stride + (int64_t)head * D * kKvPage;
+    uint8_t* scale = (is_v ? a.cache.v_scales : a.cache.k_scales) +
+                     (int64_t)page * a.cache.scale_stride + head;
+    const uint32_t was = t0 > 0 ? *scale : 0u;
+    uint32_t amax = 0;
 #pragma unroll
     for (int k = 0; k < kItems; ++k)
 #pragma unroll
@@ -100,10 +115,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
             }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off));
-    __shared__ uint32_t red[kWaves];
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
-    __syncthreads();
-    amax = max(max(red[0], red[1]), max(red[2], red[3]));
+    if constexpr (THREADS > 64) {
+        __shared__ uint32_t red[THREADS / 64];
+        if ((tid & 63) == 0) red[tid >> 6] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w) amax = max(amax, red[w]);
+    }
 
     const bool nan = amax >= 0x7F80u || was == 255u;
     uint32_t byte = (uint32_t)max((int)(amax >> 7) - 8, 0);
@@ -113,10 +131,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
     // 448 * 2^X as a BF16 pattern: larger magnitudes saturate to it
     const uint32_t cap = (byte << 7) + 0x460u;
     const u16x2 cap2 = __builtin_bit_cast(u16x2, cap | (cap << 16));
+    // The page's codes in LDS.  K's 16-byte piece of chunk c and token t at token t ^ (c % 8),
+    // V's rows 17 dwords apart: the items of a wave then write to different banks.
+    constexpr bool kWhole = QUADS == kKvPage / 4;
+    __shared__ __attribute__((aligned(16))) uint32_t image[kWhole ? D * 17 : 1];
+    const bool whole = kWhole && t0 == 0 && t1 == kKvPage;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-        const int w = (int)threadIdx.x + k * kThreads;
-        const int tq = 4 * (w / kPieces), d = 4 * (w % kPieces);
+        const int w = tid + k * THREADS;
+        const int tq = 4 * (q0 + w / kPieces), d = 4 * (w % kPieces);
+        if (tq >= t1) break;
         uint32_t c[4];                             // 4 codes of token tq + e
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -135,6 +159,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
             c[e] = nan ? 0u : __builtin_bit_cast(uint32_t, r);
         }
         if (!is_v) {
+            if (whole) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    image[(d / 16 * kKvPage + ((tq + e) ^ (d / 16 % 8))) * 4 + d % 16 / 4] = c[e];
+                continue;
+            }
             uint8_t* o = codes + (d / 16) * (16 * kKvPage) + d % 16;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -149,7 +179,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
                                       (((c[1] >> (8 * b)) & 0xFFu) << 8) |
                                       (((c[2] >> (8 * b)) & 0xFFu) << 16) |
                                       (((c[3] >> (8 * b)) & 0xFFu) << 24);
-                if (tq >= t0 && tq + 4 <= t1) {
+                if (whole) {
+                    image[(d + b) * 17 + 4 * (tq / 4 % 4) + tq / 16] = word;
+                } else if (tq >= t0 && tq + 4 <= t1) {
                     *reinterpret_cast<uint32_t*>(o + b * kKvPage) = word;
                 } else {
 #pragma unroll
@@ -160,23 +192,50 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
             }
         }
     }
-    // the tokens that were there, on the grown scale; each thread owns whole
-    // tokens of one element, apart from the bytes written above
+    if (whole) {
+        __syncthreads();
+        for (int y = tid; y < D * kKvPage / 16; y += THREADS) {
+            u32x4 o;
+            if (!is_v) {
+                const int c = y / kKvPage, t = y % kKvPage;
+                o = *reinterpret_cast<const u32x4*>(&image[(c * kKvPage + (t ^ (c % 8))) * 4]);
+            } else {
+                const uint32_t* r = &image[y / 4 * 17 + y % 4 * 4];
+                o = (u32x4){r[0], r[1], r[2], r[3]};
+            }
+            *reinterpret_cast<u32x4*>(codes + 16 * y) = o;
+        }
+    }
+    // The tokens that were there, on the grown scale, a dword at a time: four elements of a
+    // token of K, four tokens of an element of V.  Of V's group that the new tokens share,
+    // only the old tokens' bytes are written.
     if (t0 > 0 && byte != was) {
-        const float fac = nan ? 0.0f : __builtin_ldexpf(1.0f, (int)was - (int)byte);
-        for (int w = (int)threadIdx.x; w < t0 * D; w += kThreads) {
-            const int t = w / D, d = w % D;
-            uint8_t* o = is_v ? codes + d * kKvPage + 16 * (t / 4 % 4) + 4 * (t / 16) + t % 4
-                              : codes + (d / 16) * (16 * kKvPage) + t * 16 + d % 16;
-            const float f =
-                __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)*o, 1.0f, false)[0] * fac;
-            i16x2 r = {0, 0};
-            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, f, 0.0f, 1.0f, false);
-            *o = nan ? 0 : (uint8_t)__builtin_bit_cast(uint32_t, r);
+        const float f = nan ? 0.0f : __builtin_ldexpf(1.0f, (int)was - (int)byte);
+        if (!is_v) {
+#pragma unroll 4
+            for (int w = tid; w < t0 * kPieces; w += THREADS) {
+                const int t = w / kPieces, d = 4 * (w % kPieces);
+                uint32_t* o = reinterpret_cast<uint32_t*>(codes + (d / 16) * (16 * kKvPage) + t * 16 +
+                                                          d % 16);
+                *o = nan ? 0u : rescale_codes(*o, f);
+            }
+        } else {
+#pragma unroll 4
+            for (int w = tid; w < t0 / 4 * D; w += THREADS) {
+                const int q = w / D, d = w % D;
+                uint32_t* o = reinterpret_cast<uint32_t*>(codes + d * kKvPage + 16 * (q % 4) + 4 * (q / 4));
+                *o = nan ? 0u : rescale_codes(*o, f);
+            }
+            const int left = t0 % 4, q = t0 / 4;
+            for (int w = tid; w < left * D; w += THREADS) {
+                const int e = w / D, d = w % D;
+                uint8_t* o = codes + d * kKvPage + 16 * (q % 4) + 4 * (q / 4) + e;
+                *o = nan ? 0 : (uint8_t)rescale_codes(*o, f);
+            }
         }
     }
     // `was` was read by every thread before the barrier above
-    if (threadIdx.x == 0) *scale = (uint8_t)byte;
+    if (tid == 0) *scale = (uint8_t)byte;
 }
 
 // ------------------------------------------------------------ attention
@@ -231,7 +290,7 @@ template <int D, int CB>
 struct AttState {
     f32x4 acc[CB][D / 16];
     float m[CB], l[CB];              // l: the lane's share
-    int unit;
+    int unit;                        // the unit of acc
 };
 
 template <int D, int CB>
@@ -255,13 +314,17 @@ struct Columns {
 };
 
 // V's scale goes into its conversion to FP16, relative to acc's unit: exact
-// within [-15, 7] of it.  Past that the unit moves, by 60 at most towards a
-// smaller scale (acc grows by as much).
+// within [-15, 7] of it.  Past that the unit moves, but stays within 2^60 of the
+// largest scale so far: acc, at most 2^9 2^15 2^60 a token, then cannot overflow.
 __device__ __forceinline__ int v_exponent(uint32_t vs) { return vs == 255u ? 0 : (int)vs - 127; }
-__device__ __forceinline__ int next_unit(int unit, uint32_t vs) {
-    const int e = v_exponent(vs);
-    return e > unit + 7 || e < unit - 15 ? max(e, unit - 60) : unit;
-}
+struct Unit {
+    int unit = -1000, top = -1000;   // of acc; the largest scale so far
+    __device__ __forceinline__ void follow(uint32_t vs) {
+        const int e = v_exponent(vs);
+        top = max(top, e);
+        if (e > unit + 7 || e < unit - 15) unit = max(e, top - 60);
+    }
+};
 // 2^n for the n of units and scales; below the normal numbers 0.
 __device__ __forceinline__ float power_of_two(int n) {
     return n < -126 ? 0.0f : __uint_as_float((uint32_t)(min(n, 127) + 127) << 23);
@@ -502,6 +565,7 @@ attend_split_kernel(const AttendArgs a) {
 
     AttState<D, 1> st;
     init_state(st);
+    Unit unit;
     const float cc = __builtin_fabsf(a.scale) * kLog2e;
     const int64_t head_off = (int64_t)kvh * D * kKvPage;
     for (int p = from + wave; p < to; p += W) {
@@ -525,9 +589,9 @@ attend_split_kernel(const AttendArgs a) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) vr[i] = load(vb + i * 1024);
         const uint32_t ks = a.cache.k_scales[so_], vs = a.cache.v_scales[so_];
-        const int unit = next_unit(st.unit, vs);
-        if (unit != st.unit) move_unit(st, unit);
-        const float vf = v_factor(vs, unit);
+        unit.follow(vs);
+        if (unit.unit != st.unit) move_unit(st, unit.unit);
+        const float vf = v_factor(vs, unit.unit);
         if (p * kKvPage + kKvPage > sq.L) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
@@ -647,14 +711,14 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
     };
     // scale bytes and unit of the page converted last (ks 256: it was none)
     uint32_t ks = 256, vs = 0;
-    int unit = st.unit;
+    Unit unit;
     auto convert = [&](int p, bf16x8* kb, f16x8* vb) {
         ks = 256;
         if (page_in < 0) return;
         ks = __builtin_amdgcn_readfirstlane(ks_v);
         vs = __builtin_amdgcn_readfirstlane(vs_v);
-        unit = next_unit(unit, vs);
-        const float vf = v_factor(vs, unit);
+        unit.follow(vs);
+        const float vf = v_factor(vs, unit.unit);
         if (p * kKvPage + kKvPage > sq.L) {
 #pragma unroll
             for (int k = 0; k < kLoads; ++k)
@@ -681,7 +745,7 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
         // page p is in LDS, and no wave reads the other buffer any more
         __syncthreads();
         const uint32_t ks_now = ks, vs_now = vs;
-        const int unit_now = unit;
+        const int unit_now = unit.unit;
         convert(p + 1, ko, vo);
         fetch(p + 2);
         if (unit_now != st.unit) move_unit(st, unit_now);
@@ -788,18 +852,29 @@ void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
+namespace {
+template <int D>
+void append(const AppendArgs& a, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.seqs.num_seqs * a.pages_per_seq),
                     (uint32_t)a.cache.num_heads, 2);
+    // up to 5 tokens lie in two groups of 4: one wave's work
+    if (a.max_new <= 5)
+        hipLaunchKernelGGL((kv_append_kernel<D, 64, 2>), grid, dim3(64), 0, stream, a);
+    else
+        hipLaunchKernelGGL((kv_append_kernel<D, kThreads, 16>), grid, dim3(kThreads), 0, stream, a);
+}
+}  // namespace
+
+hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
     switch (a.cache.head_dim) {
-        case 64: hipLaunchKernelGGL(kv_append_kernel<64>, grid, dim3(kThreads), 0, stream, a); break;
-        case 128: hipLaunchKernelGGL(kv_append_kernel<128>, grid, dim3(kThreads), 0, stream, a); break;
-        default: hipLaunchKernelGGL(kv_append_kernel<256>, grid, dim3(kThreads), 0, stream, a); break;
+        case 64: append<64>(a, stream); break;
+        case 128: append<128>(a, stream); break;
+        default: append<256>(a, stream); break;
     }
     return hipGetLastError();
 }
 
-constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16;
+constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40;
 
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window) {
@@ -810,16 +885,18 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     p.col_blocks = (int32_t)((cols + per_block - 1) / per_block);
     int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
     if (window > 0 && window < max_kv) pages = (window + max_q) / kKvPage + 2;
-    // runs of pages: kSplitTarget workgroups if every sequence were the longest, and
-    // kSplitLeast pages at least in a run
+    // Runs of pages: kSplitTarget workgroups if every sequence were the longest, and
+    // kSplitLeast pages at least in a run.  Joining costs a second kernel (4 us), as much as a
+    // workgroup of eight waves takes for 32 pages more: up to kSplitNone nothing is split.
     const double blocks = (double)num_seqs * (double)num_heads * p.col_blocks;
     int64_t run = (int64_t)std::ceil(std::min((double)pages, (double)pages * blocks / kSplitTarget));
     if (run < kSplitLeast) run = kSplitLeast;
     run = (run + kWaves - 1) / kWaves * kWaves;
+    if (pages <= kSplitNone) run = kSplitNone;
     const int64_t splits = (pages + run - 1) / run;
     p.splits = p.rows_form || splits < 1 ? 1 : (int32_t)splits;
     // little work: eight waves share a run, so each walks half as many pages
-    p.wide = blocks * p.splits <= 256;
+    p.wide = blocks * p.splits <= 512;
     p.split_pages = (int32_t)run;
     return p;
 }

@@ -401,6 +401,9 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int
         }
         for (int c = c_from; c < c_to; ++c) {
             const auto st = load_step<FMT, CH>(w, c, a.hidden);
+            // all of the step's loads before any use: the compiler sank them past the first
+            // chunks' products (16 tokens over 256 experts, 7168 x 512: 113 us to 94)
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int at = c * S + 128 * i;

@@ -74,45 +74,65 @@ __device__ __forceinline__ Request request(const PageArgs& p, int i) {
     return r;
 }
 
-template <bool FORK>
+// SMALL: at most kScanThreads requests, one a thread, which stay in LDS; others are read
+// again where they are needed, their ranks kept in status.
+template <bool FORK, bool SMALL>
 __global__ void __launch_bounds__(kScanThreads) give_out_kernel(const PageArgs p) {
     __shared__ int tmp[kScanWaves + 1];
+    __shared__ Request kept[SMALL ? kScanThreads : 1];
+    __shared__ int ranks[SMALL ? kScanThreads : 1];
     const int tid = (int)threadIdx.x;
-    // status[i]: the rank of request i's first page, until the end
+    // the first step's counts, while the requests are read
+    int ref[4];
+    auto load_counts = [&](int64_t b0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t b = b0 + 4 * tid + k;
+            ref[k] = b < p.cache.num_pages ? p.refcounts[b] : 1;
+        }
+    };
+    load_counts(0);
+    // the rank of request i's first page
+    auto rank_of = [&](int i) { return SMALL ? ranks[i] : p.status[i]; };
+    auto request_of = [&](int i) { return SMALL ? kept[i] : request<FORK>(p, i); };
     int64_t need = 0;
     for (int i0 = 0; i0 < p.n; i0 += kScanThreads) {
         const int i = i0 + tid;
-        const int v = i < p.n ? request<FORK>(p, i).pages : 0;
+        Request r{0, 0, 0, 0};
+        if (i < p.n) r = request<FORK>(p, i);
         int total;
-        const int before = block_prefix(v, tmp, total);
+        const int before = block_prefix(r.pages, tmp, total);
         // ranks past every page stay past every page
-        if (i < p.n) p.status[i] = (int)min(need + before, (int64_t)0x7FFFFFFF);
+        const int rank = (int)min(need + before, (int64_t)0x7FFFFFFF);
+        if (SMALL) {
+            kept[tid] = r;
+            ranks[tid] = rank;
+        } else if (i < p.n) {
+            p.status[i] = rank;
+        }
         need += total;
     }
     __syncthreads();
     int64_t found = 0;
     for (int64_t b0 = 0; b0 < p.cache.num_pages && found < need; b0 += 4 * kScanThreads) {
+        if (b0 > 0) load_counts(b0);
         const int64_t b = b0 + 4 * tid;
-        bool is_free[4];
         int v = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            is_free[k] = b + k < p.cache.num_pages && p.refcounts[b + k] == 0;
-            v += is_free[k];
-        }
+        for (int k = 0; k < 4; ++k) v += ref[k] == 0;
         int total;
         int64_t rank = found + block_prefix(v, tmp, total);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (!is_free[k]) continue;
+            if (ref[k] != 0) continue;
             if (rank < need) {
                 int lo = 0, hi = p.n;              // the last request whose rank is at most this one
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) / 2;
-                    if (p.status[mid] <= rank) lo = mid; else hi = mid;
+                    if (rank_of(mid) <= rank) lo = mid; else hi = mid;
                 }
-                const Request r = request<FORK>(p, lo);
-                const int64_t at = r.first + (rank - p.status[lo]);
+                const Request r = request_of(lo);
+                const int64_t at = r.first + (rank - rank_of(lo));
                 if (!r.bad && at < p.max_pages) {
                     p.table[r.slot * p.table_stride + at] = (int32_t)(b + k);
                     p.refcounts[b + k] = 1;
@@ -124,8 +144,8 @@ __global__ void __launch_bounds__(kScanThreads) give_out_kernel(const PageArgs p
     }
     __syncthreads();
     for (int i = tid; i < p.n; i += kScanThreads) {
-        const Request r = request<FORK>(p, i);
-        const int64_t start = p.status[i];
+        const Request r = request_of(i);
+        const int64_t start = rank_of(i);
         int st = r.bad;
         if (!st && r.pages > 0 && start + r.pages > found) {
             st = 1;                                // pages it was given already go back
@@ -143,11 +163,22 @@ __global__ void __launch_bounds__(kScanThreads) give_out_kernel(const PageArgs p
     }
 }
 
+template <bool FORK>
+void give_out(const PageArgs& p, hipStream_t stream) {
+    if (p.n <= kScanThreads)
+        hipLaunchKernelGGL((give_out_kernel<FORK, true>), dim3(1), dim3(kScanThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL((give_out_kernel<FORK, false>), dim3(1), dim3(kScanThreads), 0, stream, p);
+}
+
 // Part `part` (of parts_of) of a page's copy.
 __host__ __device__ inline int parts_of(const KvCache& c) {
     const int64_t bytes = 2 * (int64_t)c.num_heads * c.head_dim * kKvPage;
     return (int)((bytes + kCopyBytes - 1) / kCopyBytes);
 }
+// AWAY: pages not read again at once pass the caches by (8192 pages of 128 KiB half in use
+// moved together in 104 us against 111).
+template <bool AWAY>
 __device__ __forceinline__ void copy_part(const KvCache& c, int64_t src, int64_t dst, int part) {
     typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
     const int64_t half = (int64_t)c.num_heads * c.head_dim * kKvPage;   // a multiple of 4096
@@ -155,16 +186,20 @@ __device__ __forceinline__ void copy_part(const KvCache& c, int64_t src, int64_t
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int64_t o = (int64_t)part * kCopyBytes + (k * kCopyThreads + (int)threadIdx.x) * 16;
-        if (o < 2 * half)
-            v[k] = *reinterpret_cast<const u32x4*>(
-                (o < half ? c.k_codes + o : c.v_codes + (o - half)) + src * c.page_stride);
+        if (o >= 2 * half) break;
+        const u32x4* from = reinterpret_cast<const u32x4*>(
+            (o < half ? c.k_codes + o : c.v_codes + (o - half)) + src * c.page_stride);
+        if constexpr (AWAY) v[k] = __builtin_nontemporal_load(from);
+        else v[k] = *from;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int64_t o = (int64_t)part * kCopyBytes + (k * kCopyThreads + (int)threadIdx.x) * 16;
-        if (o < 2 * half)
-            *reinterpret_cast<u32x4*>((o < half ? c.k_codes + o : c.v_codes + (o - half)) +
-                                      dst * c.page_stride) = v[k];
+        if (o >= 2 * half) break;
+        u32x4* to = reinterpret_cast<u32x4*>((o < half ? c.k_codes + o : c.v_codes + (o - half)) +
+                                             dst * c.page_stride);
+        if constexpr (AWAY) __builtin_nontemporal_store(v[k], to);
+        else *to = v[k];
     }
     if (part == 0)
         for (int h = (int)threadIdx.x; h < c.num_heads; h += kCopyThreads) {
@@ -178,7 +213,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PageArgs
     const int src = p.a[i], dst = p.b[i];
     if (src < 0 || src >= p.cache.num_pages || dst < 0 || dst >= p.cache.num_pages || src == dst)
         return;
-    copy_part(p.cache, src, dst, part);
+    copy_part<true>(p.cache, src, dst, part);
 }
 
 // After give_out_kernel<true>: workgroup 0 of a fork shares the full pages, the others
@@ -200,7 +235,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const PageArgs p, in
     } else if (len % kKvPage != 0) {
         const int src = from[full], dst = to[full];
         if (src >= 0 && src < p.cache.num_pages && dst >= 0 && dst < p.cache.num_pages)
-            copy_part(p.cache, src, dst, part);
+            copy_part<false>(p.cache, src, dst, part);
     }
 }
 
@@ -226,8 +261,21 @@ __global__ void __launch_bounds__(kCopyThreads) pages_free_kernel(const PageArgs
 __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const CompactArgs p) {
     __shared__ int tmp[kScanWaves + 1];
     const int tid = (int)threadIdx.x, N = p.cache.num_pages;
-    int mine = 0, live;
-    for (int64_t b = 4 * tid; b < N; b += 4 * kScanThreads)
+    // the first kKept steps' counts stay in registers
+    constexpr int kKept = 4;
+    int ref[kKept][4], mine = 0, live;
+#pragma unroll
+    for (int s = 0; s < kKept; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t i = (int64_t)s * 4 * kScanThreads + 4 * tid + k;
+            ref[s][k] = i < N ? p.refs[i] : 0;
+        }
+#pragma unroll
+    for (int s = 0; s < kKept; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mine += ref[s][k] > 0;
+    for (int64_t b = kKept * 4 * kScanThreads + 4 * tid; b < N; b += 4 * kScanThreads)
 #pragma unroll
         for (int k = 0; k < 4; ++k) mine += b + k < N && p.refs[b + k] > 0;
     block_prefix(mine, tmp, live);
@@ -235,19 +283,18 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const Compac
     int32_t* dst = src + N / 2 + 1;
     int32_t* renumber = dst + N / 2 + 1;           // of pages n and above
     int n_src = 0, n_dst = 0;
-    for (int64_t b0 = 0; b0 < N; b0 += 4 * kScanThreads) {
+    auto step = [&](int64_t b0, const int (&ref)[4]) {
         const int64_t b = b0 + 4 * tid;
         int s[4], d[4], vs = 0, vd = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int64_t i = b + k;
-            const int ref = i < N ? p.refs[i] : 0;
-            s[k] = i < N && i >= live && ref > 0;
-            d[k] = i < N && i < live && ref <= 0;
+            s[k] = i < N && i >= live && ref[k] > 0;
+            d[k] = i < N && i < live && ref[k] <= 0;
             vs += s[k];
             vd += d[k];
             if (i < N && !s[k] && !d[k]) {
-                p.refs_out[i] = i < live ? ref : 0;
+                p.refs_out[i] = i < live ? ref[k] : 0;
                 if (i >= live) renumber[i] = (int32_t)i;
             }
         }
@@ -262,6 +309,15 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const Compac
         }
         n_src += total & 0xFFFF;
         n_dst += total >> 16;
+    };
+#pragma unroll
+    for (int s = 0; s < kKept; ++s)
+        if ((int64_t)s * 4 * kScanThreads < N) step((int64_t)s * 4 * kScanThreads, ref[s]);
+    for (int64_t b0 = kKept * 4 * kScanThreads; b0 < N; b0 += 4 * kScanThreads) {
+        int more[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) more[k] = b0 + 4 * tid + k < N ? p.refs[b0 + 4 * tid + k] : 0;
+        step(b0, more);
     }
     __syncthreads();
     for (int k = tid; k < n_src; k += kScanThreads) {
@@ -298,7 +354,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const Compac
         return;
     }
     for (int64_t w = blockIdx.x - table_blocks; w < moves * parts; w += gridDim.x - table_blocks)
-        copy_part(p.cache, src[w / parts], dst[w / parts], (int)(w % parts));
+        copy_part<true>(p.cache, src[w / parts], dst[w / parts], (int)(w % parts));
 }
 
 }  // namespace
@@ -311,12 +367,12 @@ hipError_t launch_pages_copy(const PageArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_pages_reserve(const PageArgs& p, hipStream_t stream) {
-    hipLaunchKernelGGL(give_out_kernel<false>, dim3(1), dim3(kScanThreads), 0, stream, p);
+    give_out<false>(p, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_pages_fork(const PageArgs& p, hipStream_t stream) {
-    hipLaunchKernelGGL(give_out_kernel<true>, dim3(1), dim3(kScanThreads), 0, stream, p);
+    give_out<true>(p, stream);
     const int parts = parts_of(p.cache);
     hipLaunchKernelGGL(fork_kernel, dim3((uint32_t)((int64_t)p.n * (parts + 1))),
                        dim3(kCopyThreads), 0, stream, p, parts);

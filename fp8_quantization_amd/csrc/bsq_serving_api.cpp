@@ -205,6 +205,7 @@ int kv_cache_append(const bsq_kv_cache* cache, const void* k, int64_t ldk, const
     if (num_seqs * pages > kMaxInt)
         return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
     a.pages_per_seq = (int32_t)pages;
+    a.max_new = (int32_t)max_new;
     return launched(bsq::launch_kv_append(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -37,7 +37,8 @@ struct AppendArgs {
     KvSeqs seqs;
     const uint16_t* x[2];            // K, V
     int64_t ldx[2];                  // elements
-    int32_t pages_per_seq;           // grid bound on the pages a sequence's new tokens touch
+    int32_t max_new;                 // tokens of a sequence at most
+    int32_t pages_per_seq;           // grid bound on the pages that they touch
 };
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream);
 

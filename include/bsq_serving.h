@@ -112,7 +112,8 @@ int kv_cache_append(const bsq_kv_cache* cache, const void* k, int64_t ldk, const
  * of no others; bytes past a sequence's end are never used.  E4M3 NaN codes
  * inside a sequence's length (which kv_cache_append never writes) make the
  * result of that sequence's head unspecified.  A page number outside the
- * cache leaves its tokens unseen.
+ * cache leaves its tokens unseen.  Where the V scales of a head's pages lie
+ * more than 2^60 apart, the smaller ones count as 0.
  *
  * Scores, softmax statistics and sums are fp32; K and V codes enter the
  * matrix cores exactly (K as BF16 beside the BF16 queries, V as FP16), and
