@@ -672,7 +672,6 @@ __global__ void __launch_bounds__(kDownThreads, 4) moe_down_part_kernel(const Mo
             const int x = k * kDownThreads + tid;
             const int piece = x % (kStage / 8), half = x / (kStage / 8) & 1, row = x / (kStage / 4);
             const int at = p.c * S + 8 * piece;
-            hv[k] = (u32x4){0, 0, 0, 0};
             if (p.b0 + row < p.n && at < a.inter)
                 hv[k] = *reinterpret_cast<const u32x4*>(
                     a.h + ((int64_t)order[p.begin + p.b0 + row] * 2 + half) * a.inter + at);
@@ -683,7 +682,7 @@ __global__ void __launch_bounds__(kDownThreads, 4) moe_down_part_kernel(const Mo
         for (int k = 0; k < kPieces; ++k) {
             const int x = k * kDownThreads + tid;
             const int piece = x % (kStage / 8), half = x / (kStage / 8) & 1, row = x / (kStage / 4);
-            if (p.b0 + row < p.n)
+            if (p.b0 + row < p.n && p.c * S + 8 * piece < a.inter)
                 *reinterpret_cast<u32x4*>(stage + (half * 16 + row) * kStageRow + 8 * piece) = hv[k];
         }
     };
@@ -695,10 +694,10 @@ __global__ void __launch_bounds__(kDownThreads, 4) moe_down_part_kernel(const Mo
     advance(ahead, 1);
     fetch(at);
     keep(at, stage0);
-    auto step = [&](const Step<FMT, 2, CH>& st, const uint16_t* h0) {
-        // chunks past the end meet zeros of h
+    auto step = [&](const Step<FMT, 2, CH>& st, const uint16_t* h0, int c) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+            if (c * S + 128 * i >= a.inter) break;
             bf16x8 ws[2][4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) convert<FMT>(st, t, i, ws[t]);
@@ -730,7 +729,7 @@ __global__ void __launch_bounds__(kDownThreads, 4) moe_down_part_kernel(const Mo
                 s1 = load(ahead);
                 advance(ahead, 1);
             }
-            step(s0, h0 + k * S);
+            step(s0, h0 + k * S, at.c + k);
             if (at.c + k + 1 >= steps) {
                 s0 = s1;
                 break;
@@ -739,7 +738,7 @@ __global__ void __launch_bounds__(kDownThreads, 4) moe_down_part_kernel(const Mo
                 s0 = load(ahead);
                 advance(ahead, 1);
             }
-            step(s1, h0 + (k + 1) * S);
+            step(s1, h0 + (k + 1) * S, at.c + k + 1);
         }
         if (at.c + kSteps >= steps) {              // the 16 entries' last stage
             const int e = order[at.begin + at.b0 + r];
