@@ -228,12 +228,15 @@ struct FewEntries {
     float w;                         // with the weights of equal entries of the token
     uint64_t counted;                // the entries that count
 };
-__device__ __forceinline__ FewEntries few_entries(const MoeArgs& a, int id, float w) {
+// distinct: no token names an expert twice (logits routed it)
+__device__ __forceinline__ FewEntries few_entries(const MoeArgs& a, int id, float w, bool distinct) {
     const int lane = (int)threadIdx.x & 63;
     FewEntries r;
     const bool valid = lane < a.tokens * a.topk && id >= 0 && id < a.experts && w != 0.0f;
     r.id = valid ? id : -1;
     r.w = w;
+    r.counted = __ballot(valid);
+    if (distinct) return r;
     // equal entries of the token before and after this one
     const int t0 = lane - lane % a.topk;
     bool again = false;
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int
             id = a.ids[lane];
             w = a.weights[lane];
         }
-        const FewEntries e = few_entries(a, id, w);
+        const FewEntries e = few_entries(a, id, w, FROM == kRoute);
         if (!((e.counted >> unit) & 1u)) return;
         expert = expert_at(e, unit);
         few = entries_of(e, expert);
@@ -401,6 +404,17 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int
         }
         for (int c = c_from; c < c_to; ++c) {
             const auto st = load_step<FMT, CH>(w, c, a.hidden);
+            // with registers to spare, the tokens' values too
+            constexpr bool kAhead = NB == 1 && G == 1;
+            bf16x8 xa[kAhead ? CH : 1][4];
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        xa[i][s] = *reinterpret_cast<const bf16x8*>(
+                            xr[0] + min(c * S + 128 * i, a.hidden - 128) + 8 * s);
+            }
             // all of the step's loads before any use: the compiler sank them past the first
             // chunks' products (16 tokens over 256 experts, 7168 x 512: 113 us to 94)
             __builtin_amdgcn_sched_barrier(0);
@@ -412,8 +426,10 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        xs[b][s] = *reinterpret_cast<const bf16x8*>(xr[b] + at + 8 * s);
+                    for (int s = 0; s < 4; ++s) {
+                        if constexpr (kAhead) xs[b][s] = xa[i][s];
+                        else xs[b][s] = *reinterpret_cast<const bf16x8*>(xr[b] + at + 8 * s);
+                    }
 #pragma unroll
                 for (int t = 0; t < 2 * G; ++t) {
                     bf16x8 ws[4];
@@ -473,14 +489,15 @@ constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
 
 template <int FMT>
 __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArgs a) {
-    constexpr int CH = kLong<FMT>, S = 128 * CH;
+    constexpr int CH = kShort<FMT>, S = 128 * CH;
     __shared__ float sums[kDownWaves][16 * 16];    // [token][column]
     const int tid = (int)threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int entries = a.tokens * a.topk;
     for (int k = lane; k < 16 * 16; k += 64) sums[wave][k] = 0.0f;
     const FewEntries few =
-        few_entries(a, lane < entries ? a.ids[lane] : -1, lane < entries ? a.weights[lane] : 0.0f);
+        few_entries(a, lane < entries ? a.ids[lane] : -1, lane < entries ? a.weights[lane] : 0.0f,
+                    a.logits != nullptr);
     uint64_t firsts = 0;                           // the first entry of each expert
     for (uint64_t m = few.counted; m;) {
         const int at = __ffsll((unsigned long long)m) - 1;
@@ -496,53 +513,68 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
         for (int i = 0; i < ai; ++i) m &= m - 1;
         return expert_at(few, __ffsll((unsigned long long)m) - 1);
     };
-    auto load = [&](int it) {
-        const int ai = it / steps;
-        Rows<1> w;
-        set_rows<FMT>(w, 0, a.w2, a.w2_scales, (int64_t)expert_in_use(ai) * a.hidden + col0, a.inter);
-        return load_step<FMT, CH>(w, it - ai * steps, a.inter);
+    // an item's weights and h, both one item ahead of their use: h comes from other CUs' stores
+    struct Item {
+        Step<FMT, 1, CH> w;
+        bf16x8 hi[CH][4], lo[CH][4];
+        int row, n;                                // the entry of column r16; entries of the expert
     };
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto use = [&](const Step<FMT, 1, CH>& st, int it) {
-        const int ai = it / steps, c = it - ai * steps;
-        const uint64_t m = entries_of(few, expert_in_use(ai));
+    auto load = [&](int it) {
+        const int ai = it / steps, c = it - ai * steps, expert = expert_in_use(ai);
+        Item r;
+        Rows<1> w;
+        set_rows<FMT>(w, 0, a.w2, a.w2_scales, (int64_t)expert * a.hidden + col0, a.inter);
+        r.w = load_step<FMT, CH>(w, c, a.inter);
+        const uint64_t m = entries_of(few, expert);
         int row[1];
         columns_of<1>(m, 0, row);
-        const uint16_t* h0 = a.h + (int64_t)row[0] * 2 * a.inter + 32 * g;
+        r.row = row[0];
+        r.n = __popcll(m);
+        const uint16_t* h = a.h + (int64_t)r.row * 2 * a.inter + 32 * g;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int at = c * S + 128 * i;
-            if (at >= a.inter) break;
-            bf16x8 ws[4], hi[4], lo[4];
+            const int at = min(c * S + 128 * i, a.inter - 128);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                hi[s] = *reinterpret_cast<const bf16x8*>(h0 + at + 8 * s);
-                lo[s] = *reinterpret_cast<const bf16x8*>(h0 + a.inter + at + 8 * s);
+                r.hi[i][s] = *reinterpret_cast<const bf16x8*>(h + at + 8 * s);
+                r.lo[i][s] = *reinterpret_cast<const bf16x8*>(h + a.inter + at + 8 * s);
             }
-            convert<FMT>(st, 0, i, ws);
+        }
+        return r;
+    };
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto use = [&](const Item& item, int it) {
+        const int ai = it / steps, c = it - ai * steps;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            if (c * S + 128 * i >= a.inter) break;
+            bf16x8 ws[4];
+            convert<FMT>(item.w, 0, i, ws);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[s], hi[s], acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[s], lo[s], acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[s], item.hi[i][s], acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ws[s], item.lo[i][s], acc, 0, 0, 0);
             }
         }
         // the expert's (or the wave's) last step: its part goes to the tokens' sums
         if (it + 1 < it_to && it + 1 < (ai + 1) * steps) return;
-        const float f = __shfl(few.w, row[0]);
-        if (r16 < __popcll(m)) {
-            f32x4* s = reinterpret_cast<f32x4*>(&sums[wave][row[0] / a.topk * 16 + 4 * g]);
+        const float f = __shfl(few.w, item.row);
+        if (r16 < item.n) {
+            f32x4* s = reinterpret_cast<f32x4*>(&sums[wave][item.row / a.topk * 16 + 4 * g]);
             *s = *s + acc * f;
         }
         acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     };
     if (it_from < it_to) {
-        Step<FMT, 1, CH> s0 = load(it_from), s1;
+        Item s0 = load(it_from), s1;
         for (int it = it_from;; it += 2) {
             // past the wave's last item its loads repeat that item's
             s1 = load(min(it + 1, it_to - 1));
+            __builtin_amdgcn_sched_barrier(0);
             use(s0, it);
             if (it + 1 >= it_to) break;
             s0 = load(min(it + 2, it_to - 1));
+            __builtin_amdgcn_sched_barrier(0);
             use(s1, it + 1);
             if (it + 2 >= it_to) break;
         }
