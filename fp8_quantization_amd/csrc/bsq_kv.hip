@@ -372,6 +372,16 @@ __device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<C
             for (int cb = 0; cb < CB; ++cb)
                 s[cb][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[cb][k], s[cb][j], 0, 0, 0);
         }
+    if constexpr (CB > 1) {
+        // K comes from LDS: six reads ahead of the products, not two (2% of a prompt)
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+        for (int x = 0; x < D / 8 - 6; ++x) {
+            __builtin_amdgcn_sched_group_barrier(0x008, CB, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, CB * 6, 0);
+    }
     // to units of log 2; a NaN scale of K or V makes NaN of every weight it meets
     float c = c0 * __builtin_ldexpf(1.0f, (int)ks - 127);
     if (ks == 255u || vs == 255u) c = NAN;
@@ -494,6 +504,14 @@ __device__ __forceinline__ void page_range(const AttendArgs& a, const Seq& sq, i
     if (p1 < p0) p1 = p0;
 }
 
+// A split's part of them: runs of split_pages pages; the last split takes what is left,
+// however many.
+__device__ __forceinline__ void split_range(const AttendArgs& a, int split, int& p0, int& p1) {
+    const int64_t run = p0 + (int64_t)split * a.split_pages;
+    if (split + 1 < a.splits) p1 = (int)min((int64_t)p1, run + a.split_pages);
+    p0 = (int)min((int64_t)p1, run);
+}
+
 // The result of a column: O = acc 2^unit / l, or the partial sums of a split.
 template <int D>
 __device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq, int kvh, int c,
@@ -552,10 +570,8 @@ attend_split_kernel(const AttendArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int p0, p1;
     page_range(a, sq, c0, min(c0 + 16, cols) - 1, p0, p1);
-    // runs of split_pages pages; the last split takes what is left, however many
-    const int64_t run = (int64_t)split * a.split_pages;
-    const int from = (int)min((int64_t)p1, p0 + run);
-    const int to = split + 1 == a.splits ? p1 : (int)min((int64_t)p1, p0 + run + a.split_pages);
+    int from = p0, to = p1;
+    split_range(a, split, from, to);
     if (split > 0 && from >= to) return;           // nor does the join look at it
     const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
     int32_t next = from + wave < to ? row[from + wave] : 0;
@@ -662,7 +678,8 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
     b /= (uint32_t)a.cache.num_heads;
     // the last rows, which see the most tokens, first
     const int blk = a.col_blocks - 1 - (int)(b % (uint32_t)a.col_blocks);
-    const int s = (int)(b / (uint32_t)a.col_blocks);
+    b /= (uint32_t)a.col_blocks;
+    const int split = (int)(b % (uint32_t)a.splits), s = (int)(b / (uint32_t)a.splits);
     const Seq sq = load_seq(a.seqs, s);
     const int cols = (int)min((int64_t)sq.n * a.group, (int64_t)0x7FFFFFF0);
     const int tid = (int)threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
@@ -677,6 +694,10 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
     int p0, p1, q0 = 0, q1 = 0;                    // the workgroup's pages, the wave's
     page_range(a, sq, w0, min(w0 + 16 * CB * W, cols) - 1, p0, p1);
     if (mine) page_range(a, sq, c0, min(c0 + 16 * CB, cols) - 1, q0, q1);
+    if (a.splits > 1) {
+        split_range(a, split, p0, p1);
+        if (split > 0 && p0 >= p1) return;         // nor does the join look at it
+    }
     AttState<D, CB> st;
     init_state(st);
     const float cc = __builtin_fabsf(a.scale) * kLog2e;
@@ -766,87 +787,142 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
         const float f = __builtin_ldexpf(1.0f, max(st.unit - (int)kShift, -200));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) st.acc[cb][i] *= f;
-        store_column<D>(a, sq, kvh, c0 + 16 * cb + r, cols, 0, st.acc[cb], st.m[cb], l);
+        store_column<D>(a, sq, kvh, c0 + 16 * cb + r, cols, split, st.acc[cb], st.m[cb], l);
     }
 }
 
-// Joins the splits' partial results: a workgroup per (row, head).  Wave w takes
-// the splits w, w + 4, ..., a lane D / 64 consecutive elements; the waves' sums
-// are added in their order.
-template <int D>
+// Joins the splits' partial results: W waves per (row, head), a lane D / 64 consecutive
+// elements.  Wave w takes the splits w, w + W, ..., and the waves' sums are added in their
+// order.  The weights of 64 splits are found at once, a lane each, while the first sums are on
+// their way.  Both sides of kJoinAlone: 64 rows of 32 heads of 128, few splits each, take 4.7 us
+// with a wave for a pair and 8.6 with four; 4 rows of 32 heads over 32 splits 12.0 and 6.3.
+template <int D, int W>
 __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a) {
-    constexpr int E = D / 64;
+    constexpr int E = D / 64, kAhead = 8;
     __shared__ float so[kWaves][D], sl[kWaves];
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int head = (int)(blockIdx.x % (uint32_t)a.num_q_heads);
-    const uint32_t si = blockIdx.x / (uint32_t)a.num_q_heads;
+    const uint32_t pair = W == 1 ? blockIdx.x * kWaves + wave : blockIdx.x;
+    const int first = W == 1 ? 0 : wave;
+    const int head = (int)(pair % (uint32_t)a.num_q_heads);
+    const uint32_t si = pair / (uint32_t)a.num_q_heads;
     const int i = (int)(si % (uint32_t)a.max_q), s = (int)(si / (uint32_t)a.max_q);
+    if (s >= a.seqs.num_seqs) return;              // the last workgroup of W == 1
     const Seq sq = load_seq(a.seqs, s);
     if (i >= sq.n) return;
     // splits past the sequence's pages hold nothing and are not read
-    const int c0 = (i * a.group + head % a.group) / 16 * 16;
+    const int c0 = (i * a.group + head % a.group) / a.block_cols * a.block_cols;
     int p0, p1;
-    page_range(a, sq, c0, (int)min((int64_t)c0 + 16, (int64_t)sq.n * a.group) - 1, p0, p1);
+    page_range(a, sq, c0, (int)min((int64_t)c0 + a.block_cols, (int64_t)sq.n * a.group) - 1, p0, p1);
     const int used = (int)min((int64_t)a.splits,
                               ((int64_t)p1 - p0 + a.split_pages - 1) / a.split_pages);
     const int64_t row = sq.lo + i, at = row * a.num_q_heads + head;
     const int64_t stride = a.seqs.num_rows * a.num_q_heads;
-    float m = -INFINITY;
-    for (int k = lane; k < used; k += 64) m = fmaxf(m, a.part_ml[2 * (at + k * stride)]);
+    const float* part = a.part_o + at * D + lane * E;
+    const float* ml = a.part_ml + 2 * at;
+    float next[kAhead][E];
+    const auto load = [&](int k0) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int k = k0 + x * W;
+#pragma unroll
+            for (int e = 0; e < E; ++e) next[x][e] = k < used ? part[k * stride * D + e] : 0.0f;
+        }
+    };
+    load(first);
+    float m = -INFINITY, mk = -INFINITY, lk = 0.0f;    // mk, lk: of split `lane`
+    if (lane < used) {
+        m = mk = ml[2 * lane * stride];
+        lk = ml[2 * lane * stride + 1];
+    }
+    for (int k = lane + 64; k < used; k += 64) m = fmaxf(m, ml[2 * k * stride]);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
     const float ms = m == -INFINITY ? 0.0f : m;
     float l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (int k = wave; k < used; k += kWaves) {
-        const int64_t p = at + k * stride;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ms);
-        l += a.part_ml[2 * p + 1] * f;
+    float f = __builtin_amdgcn_exp2f(mk - ms);         // 0 past the last split
+    lk *= f;
+    for (int k0 = first;;) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += a.part_o[p * D + lane * E + e] * f;
+        for (int x = 0; x < kAhead; ++x) {
+            const int k = (k0 + x * W) & 63;
+            l += __shfl(lk, k);
+            const float w = __shfl(f, k);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += next[x][e] * w;
+        }
+        k0 += kAhead * W;                              // divides 64
+        if (k0 - first >= used) break;
+        load(k0);
+        if (k0 == first + (k0 & ~63)) {                // the next 64 splits' weights
+            const int k = k0 - first + lane;
+            f = k < used ? __builtin_amdgcn_exp2f(ml[2 * k * stride] - ms) : 0.0f;
+            lk = k < used ? ml[2 * k * stride + 1] * f : 0.0f;
+        }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[wave][lane * E + e] = o[e];
-    if (lane == 0) sl[wave] = l;
-    __syncthreads();
-    l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     __bf16* dst = reinterpret_cast<__bf16*>(a.out) + row * a.ldo + (int64_t)head * D;
-    for (int d = (int)threadIdx.x; d < D; d += kThreads)
-        dst[d] = (__bf16)(((so[0][d] + so[1][d]) + (so[2][d] + so[3][d])) * inv);
-    if (a.lse && threadIdx.x == 0)
+    if constexpr (W == 1) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dst[lane * E + e] = (__bf16)(o[e] * inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[wave][lane * E + e] = o[e];
+        if (lane == 0) sl[wave] = l;
+        __syncthreads();
+        l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        for (int d = (int)threadIdx.x; d < D; d += kThreads)
+            dst[d] = (__bf16)(((so[0][d] + so[1][d]) + (so[2][d] + so[3][d])) * inv);
+    }
+    if (a.lse && (W == 1 ? lane : (int)threadIdx.x) == 0)
         a.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// 16-column blocks of a wave and waves of a workgroup of the rows form (D = 256: one
-// block's sums fill the registers that two do at 128), 128 columns in all
+// 16-column blocks of a wave of the rows form (D = 256: one block's sums fill the registers
+// that two do at 128), and columns of its workgroup, narrow and wide.  A wide one's eight
+// waves share the conversion of a page, half the work of two narrow ones, but end together:
+// with 32 heads of 128, 2 sequences of 2048 rows in 8192 tokens (512 wide workgroups) take
+// 368 us wide and 398 narrow, 2 of 1024 in 4000 (256) 123 and 112.  head_dim 64 is narrow (its
+// page is too small for 512 threads), 256 has eight waves at 128 columns.
 template <int D>
 constexpr int kRowBlocks = D == 256 ? 1 : 2;
-constexpr int kRowColumns = 128;
+constexpr int kRowColumns = 128, kWideColumns = 256;
+
+constexpr int64_t kJoinAlone = 1024;
+
+template <int D, int W>
+void attend_rows(const AttendArgs& a, dim3 grid, hipStream_t stream) {
+    hipLaunchKernelGGL((attend_rows_kernel<D, kRowBlocks<D>, W>), grid, dim3(64 * W), 0, stream, a);
+}
 
 template <int D>
 void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
     const int64_t per = (int64_t)a.seqs.num_seqs * a.cache.num_heads * a.col_blocks;
-    if (p.rows_form) {
-        constexpr int W = kRowColumns / 16 / kRowBlocks<D>;
-        hipLaunchKernelGGL((attend_rows_kernel<D, kRowBlocks<D>, W>), dim3((uint32_t)per),
-                           dim3(64 * W), 0, stream, a);
-        return;
-    }
     const dim3 grid((uint32_t)(per * a.splits));
-    if (p.wide)
+    if (p.rows_form) {
+        if constexpr (D == 256) attend_rows<D, 8>(a, grid, stream);
+        else if constexpr (D == 64) attend_rows<D, 4>(a, grid, stream);
+        else if (p.wide) attend_rows<D, 8>(a, grid, stream);
+        else attend_rows<D, 4>(a, grid, stream);
+    } else if (p.wide) {
         hipLaunchKernelGGL((attend_split_kernel<D, 8, false>), grid, dim3(512), 0, stream, a);
-    else if (a.col_blocks == 1)
+    } else if (a.col_blocks == 1) {
         hipLaunchKernelGGL((attend_split_kernel<D, 4, true>), grid, dim3(256), 0, stream, a);
-    else
+    } else {
         hipLaunchKernelGGL((attend_split_kernel<D, 4, false>), grid, dim3(256), 0, stream, a);
+    }
     if (a.splits > 1) {
         const int64_t pairs = (int64_t)a.seqs.num_seqs * a.max_q * a.num_q_heads;
-        hipLaunchKernelGGL((attend_join_kernel<D>), dim3((uint32_t)pairs), dim3(kThreads), 0, stream,
-                           a);
+        if (pairs >= kJoinAlone)
+            hipLaunchKernelGGL((attend_join_kernel<D, 1>),
+                               dim3((uint32_t)((pairs + kWaves - 1) / kWaves)), dim3(kThreads), 0,
+                               stream, a);
+        else
+            hipLaunchKernelGGL((attend_join_kernel<D, kWaves>), dim3((uint32_t)pairs),
+                               dim3(kThreads), 0, stream, a);
     }
 }
 
@@ -874,29 +950,44 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40;
+constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40,
+                  kRowsLeast = 8, kRowsTarget = 512, kRowsFull = 128;
 
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window) {
     const int64_t cols = max_q * (num_q_heads / num_heads);
-    AttendPlan p;
+    AttendPlan p{};
     p.rows_form = cols > 64;
-    const int64_t per_block = p.rows_form ? kRowColumns : 16;
-    p.col_blocks = (int32_t)((cols + per_block - 1) / per_block);
     int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
     if (window > 0 && window < max_kv) pages = (window + max_q) / kKvPage + 2;
-    // Runs of pages: kSplitTarget workgroups if every sequence were the longest, and
-    // kSplitLeast pages at least in a run.  Joining costs a second kernel (4 us), as much as a
-    // workgroup of eight waves takes for 32 pages more: up to kSplitNone nothing is split.
-    const double blocks = (double)num_seqs * (double)num_heads * p.col_blocks;
-    int64_t run = (int64_t)std::ceil(std::min((double)pages, (double)pages * blocks / kSplitTarget));
-    if (run < kSplitLeast) run = kSplitLeast;
-    run = (run + kWaves - 1) / kWaves * kWaves;
-    if (pages <= kSplitNone) run = kSplitNone;
+    const double heads = (double)num_seqs * (double)num_heads;
+    p.block_cols = p.rows_form ? kRowColumns : 16;
+    if (p.rows_form) {
+        p.wide = head_dim == 128 && heads * (double)(cols / kWideColumns) >= 512;
+        if (p.wide) p.block_cols = kWideColumns;
+    }
+    p.col_blocks = (int32_t)((cols + p.block_cols - 1) / p.block_cols);
+    // Runs of pages: as many as give `target` workgroups if every sequence were the longest, of
+    // `least` pages at least.  Joining costs a second kernel (4 us and more), as much as a
+    // workgroup of the split form takes for 32 pages more: up to kSplitNone it splits nothing.
+    // The rows form, which has more sums to join, splits where it leaves half the CUs without a
+    // workgroup: 100 rows of 8 heads in 6000 tokens 25 us, unsplit 144; 2 x 500 rows of 16 heads
+    // of 64 in 3000 tokens (128 workgroups) 40 and 55; but 256 workgroups 151 and 123.
+    const double blocks = heads * p.col_blocks;
+    const double target = p.rows_form ? kRowsTarget : kSplitTarget;
+    const int64_t least = p.rows_form ? kRowsLeast : kSplitLeast;
+    int64_t run = (int64_t)std::ceil(std::min((double)pages, (double)pages * blocks / target));
+    if (run < least) run = least;
+    if (p.rows_form) {
+        if (blocks > kRowsFull) run = pages + 1;
+    } else {
+        run = (run + kWaves - 1) / kWaves * kWaves;
+        if (pages <= kSplitNone) run = kSplitNone;
+    }
     const int64_t splits = (pages + run - 1) / run;
-    p.splits = p.rows_form || splits < 1 ? 1 : (int32_t)splits;
+    p.splits = splits < 1 ? 1 : (int32_t)splits;
     // little work: eight waves share a run, so each walks half as many pages
-    p.wide = blocks * p.splits <= 512;
+    if (!p.rows_form) p.wide = blocks * p.splits <= 512;
     p.split_pages = (int32_t)run;
     return p;
 }

@@ -262,6 +262,7 @@ int kv_cache_attention(const bsq_kv_cache* cache, const void* q, int64_t ldq, in
     a.group = (int32_t)(num_q_heads / cache->num_heads);
     a.max_q = (int32_t)max_q;
     a.col_blocks = p.col_blocks;
+    a.block_cols = p.block_cols;
     a.splits = p.splits;
     a.split_pages = p.split_pages;
     return launched(bsq::launch_kv_attend(a, p, static_cast<hipStream_t>(stream)));

@@ -57,7 +57,8 @@ struct AttendArgs {
     int32_t num_q_heads;
     int32_t group;                   // num_q_heads / num_heads
     int32_t max_q;
-    int32_t col_blocks;              // workgroups over (row, head of the group) pairs
+    int32_t col_blocks;              // workgroups over (row, head of the group) pairs, and
+    int32_t block_cols;              // pairs of each
     int32_t splits;
     int32_t split_pages;             // pages of a split
 };
@@ -65,9 +66,10 @@ struct AttendArgs {
 struct AttendPlan {
     bool rows_form;                  // waves share the pages and split the columns (many rows)
     int32_t col_blocks;
+    int32_t block_cols;
     int32_t splits;
     int32_t split_pages;
-    bool wide;                       // eight waves a workgroup instead of four
+    bool wide;                       // eight waves a workgroup instead of four (both forms)
 };
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window);

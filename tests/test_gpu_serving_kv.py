@@ -230,6 +230,25 @@ def test_split_over_the_tokens(bsq, rows, kv):
     check(bsq, c, q, off, lens, table, D ** -0.5, window=2777)
 
 
+def test_more_than_64_splits(bsq):
+    D, lens = 64, [75000, 64 * 16 * 65 + 1]
+    c, q, off, table = make(5, lens, [1, 2], 1, 2, D)
+    check(bsq, c, q, off, lens, table, D ** -0.5)
+
+
+@pytest.mark.parametrize("D,hq,heads", [(64, 4, 2), (128, 2, 1), (256, 6, 1)])
+@pytest.mark.parametrize("rows", [70, 300])
+def test_many_rows_split_over_the_tokens(bsq, D, hq, heads, rows):
+    """Too few rows for every CU: their pages are split too.  Up to and over 1024 pairs of a
+    row and a head, which are joined by four waves and by one."""
+    lens, n = [2500, 40, 1030], [rows, 3, rows - 5]
+    c, q, off, table = make(D + rows, lens, n, heads, hq, D)
+    check(bsq, c, q, off, lens, table, D ** -0.5)
+    check(bsq, c, q, off, lens, table, D ** -0.5, max_kv=600)
+    check(bsq, c, q, off, lens, table, D ** -0.5, max_kv=20000)
+    check(bsq, c, q, off, lens, table, D ** -0.5, window=1111)
+
+
 @pytest.mark.parametrize("rows", [1, 90])
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0, 1e-30])
 def test_scales_of_the_scores(bsq, rows, scale):

@@ -142,7 +142,8 @@ def test_attention_workspace(lib):
     big = w(2, 128, 4, 2, 8, 1, 100000, 0)
     assert big > 0 and big % (8 * 4 * 130 * 4) == 0             # splits * rows * heads * (D + 2) floats
     assert w(2, 128, 4, 2, 8, 1, 100000, 300) == 0              # a window leaves little to split
-    assert w(2, 128, 4, 2, 2000, 1000, 100000, 0) == 0          # rows enough without splitting
+    assert w(2, 128, 4, 200, 40000, 200, 100000, 0) == 0        # rows enough without splitting
+    assert w(2, 128, 4, 1, 100, 100, 100000, 0) > 0             # many rows, but not for every CU
     assert w(0, 128, 4, 2, 8, 1, 500, 0) == -1
     assert w(2, 100, 4, 2, 8, 1, 500, 0) == -1
     assert w(2, 128, 4, 2, -1, 1, 500, 0) == -1
