@@ -50,8 +50,8 @@ __device__ __forceinline__ Seq load_seq(const KvSeqs& q, int s) {
 // so the same item serves both layouts and every store but those of a partial
 // group of tokens is a dword.  A page that is filled whole goes through LDS and
 // leaves in 16-byte stores (from the items' dwords, V's each in a line of its
-// own, 16384 tokens of 8 heads of 128 took XX us, this way YY).  A few tokens a
-// sequence (decode) take one wave and no barrier.
+// own, 16384 tokens of 8 heads of 128 took 19.7 us, this way 15.9: 4.2 TB/s).  A
+// few tokens a sequence (decode) take one wave and no barrier.
 
 // Four E4M3 codes times a power of two, rounded to E4M3 again.
 __device__ __forceinline__ uint32_t rescale_codes(uint32_t v, float f) {
@@ -550,7 +550,9 @@ __device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq,
 // Few columns (decode): a workgroup takes 16 columns of one (sequence, head)
 // and a run of their pages, its W waves every W-th page; their states meet
 // in LDS at the end.  ONCE: no other workgroup reads these pages (one block of
-// columns), so they are loaded past the caches' retention.
+// columns), so they are loaded past the caches' retention.  Bound by the pages'
+// bytes: 64 sequences of 8192 tokens, 32 heads on 8 of 128, take 111 us (6.1
+// TB/s; 132 without ONCE).
 template <int D, int W, bool ONCE>
 __global__ void __launch_bounds__(64 * W, D == 256 ? 1 : W == 4 ? 3 : 2)
 attend_split_kernel(const AttendArgs a) {
@@ -667,7 +669,9 @@ attend_split_kernel(const AttendArgs a) {
 // itself, the conversions were half of the vector instructions.  In LDS K is
 // [element / 8][token][8] and V [place / 8][element][8], the matrix
 // instruction's 16-byte operands: 16 lanes read 256 consecutive bytes, and
-// write as many (each wave's 1 KiB of V is dealt to its lanes by columns).
+// write as many (each wave's 1 KiB of V is dealt to its lanes by columns).  Bound
+// by the vector instructions of the softmax beside the matrix cores: 2 x 2048
+// rows in 8192 tokens, 32 heads of 128, reach 1.05 PFLOP/s (342 us).
 template <int D, int CB, int W>
 __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs a) {
     constexpr int kHalf = D * kKvPage, kT = 64 * W, kLoads = kHalf / (kT * 16);
@@ -933,7 +937,8 @@ template <int D>
 void append(const AppendArgs& a, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.seqs.num_seqs * a.pages_per_seq),
                     (uint32_t)a.cache.num_heads, 2);
-    // up to 5 tokens lie in two groups of 4: one wave's work
+    // up to 5 tokens lie in two groups of 4: one wave's work (64 sequences of 5 tokens, 8 heads
+    // of 128: 6.2 us a call, with 256 threads 8.1)
     if (a.max_new <= 5)
         hipLaunchKernelGGL((kv_append_kernel<D, 64, 2>), grid, dim3(64), 0, stream, a);
     else
@@ -950,8 +955,12 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40,
-                  kRowsLeast = 8, kRowsTarget = 512, kRowsFull = 128;
+// How work is split, with 32 heads of 128 on 8.  Target: 64 sequences of 8192 tokens 115 us a
+// call (1024: 128, 4096: 114).  Least: 4 of 6000 tokens 14.3 us (8: 18.1, 32: 16.8).  None:
+// 16 sequences of 5 rows in a window of 1024, 8 heads of 64, 8.4 us (split 12.8).  kRowsLeast
+// and kRowsTarget: 100 rows of 8 heads in 6000 tokens 25 us (16 pages at least: 35).
+constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40;
+constexpr int64_t kRowsLeast = 8, kRowsTarget = 512, kRowsFull = 128;
 
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window) {
@@ -986,7 +995,8 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     }
     const int64_t splits = (pages + run - 1) / run;
     p.splits = splits < 1 ? 1 : (int32_t)splits;
-    // little work: eight waves share a run, so each walks half as many pages
+    // little work: eight waves share a run, so each walks half as many pages (8 sequences of 777
+    // tokens 8.8 us, with four 10.8; 64 of 8192 145 and 115)
     if (!p.rows_form) p.wide = blocks * p.splits <= 512;
     p.split_pages = (int32_t)run;
     return p;

@@ -282,7 +282,8 @@ __device__ __forceinline__ bool counts(const int16_t* ids, int r, int topk) {
 
 // How a workgroup knows its expert and the expert's entries:
 //  kRoute  few entries, from logits, for at most kUpWaves tokens: every workgroup
-//          routes them itself, a wave each
+//          routes them itself, a wave each (one token 18.5 us a call, with a
+//          kernel to route it 20.9)
 //  kFew    few entries, from topk_ids
 //  kEntry  a workgroup per entry of topk_ids
 //  kExpert a workgroup per expert (more entries than experts)
@@ -596,9 +597,10 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
 // wave for its 32 columns it was four times the weights' loads).  While a stage
 // is computed, the next one's h and the next steps' weights are on their way,
 // over the ends of experts too: a workgroup for each expert spent its life
-// waiting for its first loads (92 us, this form XX, of which the weights at
-// 6 TB/s are 33).  The parts, times the tokens' weights, go to memory in 32
-// bits, a row an entry, and a third kernel adds a token's rows in their order.
+// waiting for its first loads (128 entries, 101 experts of 7168 x 512 in FP4:
+// 92 us, this form 56, of which the weights at 6.2 TB/s are 32).  The parts,
+// times the tokens' weights, go to memory in 32 bits, a row an entry, and a
+// third kernel adds a token's rows in their order.
 
 constexpr int kStage = 512;          // elements of h in LDS
 // 16 bytes more than a multiple of the banks' 256: 16 rows' pieces fall in different banks
@@ -846,8 +848,10 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL(moe_route_kernel, dim3((uint32_t)a.tokens), dim3(64), 0, stream, a);
         routed = true;
     }
-    // wide tiles where there are workgroups enough for every CU
-    if (units * (a.inter / 32) >= 1024) {
+    // Wide tiles (x read once for twice the weights) where they give workgroups enough: 16 tokens
+    // (1536 wide tiles, 2048 x 768) 71.8 us and 79.2 narrow, 4 (768) 35.5 and 38.2; but 1 token
+    // (128, 7168 x 512) 34.4 and 28.2.
+    if (units * (a.inter / 32) >= 768) {
         if (a.tokens <= 16) launch_up<FMT, 1, 2>(a, few, routed, stream);
         else launch_up<FMT, 2, 2>(a, few, routed, stream);
     } else {

@@ -75,7 +75,8 @@ __device__ __forceinline__ Request request(const PageArgs& p, int i) {
 }
 
 // SMALL: at most kScanThreads requests, one a thread, which stay in LDS; others are read
-// again where they are needed, their ranks kept in status.
+// again where they are needed, their ranks kept in status (32 requests: 6.4 us against 7.9).
+// A chain of dependent loads and barriers bounds it, not its bytes.
 template <bool FORK, bool SMALL>
 __global__ void __launch_bounds__(kScanThreads) give_out_kernel(const PageArgs p) {
     __shared__ int tmp[kScanWaves + 1];

@@ -13,6 +13,7 @@
  * contents (offsets, lengths, page and expert numbers) are not read on the
  * host; a number that falls outside the sizes given makes the kernels skip
  * what it names, never access memory outside the buffers.
+ * bsq_time_next_launch does not see this library's kernels.
  */
 #ifndef BSQ_SERVING_H
 #define BSQ_SERVING_H
@@ -157,9 +158,10 @@ int64_t kv_cache_attention_workspace(int64_t num_heads, int64_t head_dim, int64_
  * the inputs alone.  Slot numbers index the rows of block_table and kv_lens
  * (num_seqs of them); a request with a slot outside them fails.
  * Status codes (int32, one per request): 0 done, 1 not enough free pages or
- * table entries (nothing changed for that request), 2 a slot outside the
- * table.  One call names a slot once (children of a fork: distinct slots
- * that no request names as a parent).
+ * table entries (its length and the counts stay as they were; table entries
+ * past its end may be written), 2 a slot outside the table.  One call names a
+ * slot once (children of a fork: distinct slots that no request names as a
+ * parent).
  *
  * kv_pages_copy     page dst[i] becomes a copy of page src[i] (codes and
  *     scales of every head).  Distinct destinations, none of them a source
@@ -204,8 +206,8 @@ int kv_pages_compact(const bsq_kv_cache* cache, const int32_t* block_table, int6
 int64_t kv_pages_compact_workspace(int64_t num_pages);
 
 /*
- * A mixture-of-experts layer for a few tokens.  With at most 16 tokens and 64
- * (token, expert) entries it is two kernels: routing (of at most 4 tokens),
+ * A mixture-of-experts layer for a few tokens.  With at most 16 (token,
+ * expert) entries it is two kernels: routing (of at most 4 tokens),
  * gate and up products with the SiLU gate, then the down products summed over
  * each token's experts.  More entries keep their parts of the down products
  * apart, which a third kernel sums; more tokens are routed by one before.

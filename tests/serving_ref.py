@@ -322,7 +322,6 @@ def moe(x, ids, weights, w1, w3, w2):
     within 2^-20 of itself; h kept to 16 bits (2^-16); weights 2^-22; y rounded to BF16."""
     T, H = x.shape
     y, b = np.zeros((T, H)), np.zeros((T, H))
-    E = None
     for t in range(T):
         for j in range(ids.shape[1]):
             e, w = int(ids[t, j]), float(weights[t, j])
@@ -339,7 +338,6 @@ def moe(x, ids, weights, w1, w3, w2):
             y[t] += w * (C @ h)
             b[t] += abs(w) * (np.abs(C) @ (eh + (2 * I + 32) * 2.0 ** -24 * (np.abs(h) + eh)))
             b[t] += abs(w) * 2.0 ** -20 * np.abs(C) @ np.abs(h)
-    del E
     return y, (b + np.abs(y) * 2.0 ** -8) * (1 + 2.0 ** -7) + 2.0 ** -133
 
 
