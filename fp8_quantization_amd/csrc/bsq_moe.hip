@@ -73,7 +73,7 @@ __device__ __forceinline__ Step<FMT, NT, CH> load_step(const Rows<NT>& p, int c,
             const u32x4* w = reinterpret_cast<const u32x4*>(
                 p.w[t] + (int64_t)min(c * CH + i, K / 128 - 1) * (64 * L));
 #pragma unroll
-            for (int k = 0; k < L; ++k) r.w[t][L * i + k] = __builtin_nontemporal_load(w + k);
+            for (int k = 0; k < L; ++k) r.w[t][L * i + k] = w[k];
         }
         const uint8_t* s = p.s[t] + (int64_t)(c * CH >> 2) * 256 + (c * CH & 3);
         if constexpr (CH == 4) r.s[t] = *reinterpret_cast<const uint32_t*>(s);
@@ -848,14 +848,18 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL(moe_route_kernel, dim3((uint32_t)a.tokens), dim3(64), 0, stream, a);
         routed = true;
     }
+    // One block of 16 entries, whose waves are more at a time, unless experts commonly have more:
+    // they would read their weights again.  64 tokens, 4096 x 1024 in E4M3: 4 of 64 experts (4 an
+    // expert) 172 us and 181 with two, 2 of 8 (16 an expert) 68 and 62.
+    const bool narrow = a.tokens <= 16 || entries <= 10 * a.experts;
     // Wide tiles (x read once for twice the weights) where they give workgroups enough: 16 tokens
     // (1536 wide tiles, 2048 x 768) 71.8 us and 79.2 narrow, 4 (768) 35.5 and 38.2; but 1 token
     // (128, 7168 x 512) 34.4 and 28.2.
     if (units * (a.inter / 32) >= 768) {
-        if (a.tokens <= 16) launch_up<FMT, 1, 2>(a, few, routed, stream);
+        if (narrow) launch_up<FMT, 1, 2>(a, few, routed, stream);
         else launch_up<FMT, 2, 2>(a, few, routed, stream);
     } else {
-        if (a.tokens <= 16) launch_up<FMT, 1, 1>(a, few, routed, stream);
+        if (narrow) launch_up<FMT, 1, 1>(a, few, routed, stream);
         else launch_up<FMT, 2, 1>(a, few, routed, stream);
     }
     if (few) {
