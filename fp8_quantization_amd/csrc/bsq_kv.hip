@@ -671,7 +671,7 @@ attend_split_kernel(const AttendArgs a) {
 // instruction's 16-byte operands: 16 lanes read 256 consecutive bytes, and
 // write as many (each wave's 1 KiB of V is dealt to its lanes by columns).  Bound
 // by the vector instructions of the softmax beside the matrix cores: 2 x 2048
-// rows in 8192 tokens, 32 heads of 128, reach 1.05 PFLOP/s (342 us).
+// rows in 8192 tokens, 32 heads of 128, reach 1.06 PFLOP/s (339 us).
 template <int D, int CB, int W>
 __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs a) {
     constexpr int kHalf = D * kKvPage, kT = 64 * W, kLoads = kHalf / (kT * 16);

@@ -61,7 +61,8 @@ __device__ __forceinline__ void set_rows(Rows<NT>& p, int t, const uint8_t* code
     p.s[t] = scales + row / 16 * ((int64_t)((K + 511) / 512) * 256) + 4 * lane;
 }
 
-// Step c; chunks past the row's end repeat its last one.
+// Step c; chunks past the row's end repeat its last one.  Through the caches: two loads share
+// each line (past them 64 tokens of 4 of 64 experts took 172 us, this way 158).
 template <int FMT, int CH, int NT>
 __device__ __forceinline__ Step<FMT, NT, CH> load_step(const Rows<NT>& p, int c, int K) {
     constexpr int L = kLoads<FMT>;
@@ -282,8 +283,8 @@ __device__ __forceinline__ bool counts(const int16_t* ids, int r, int topk) {
 
 // How a workgroup knows its expert and the expert's entries:
 //  kRoute  few entries, from logits, for at most kUpWaves tokens: every workgroup
-//          routes them itself, a wave each (one token 18.5 us a call, with a
-//          kernel to route it 20.9)
+//          routes them itself, a wave each (one token 17.3 us a call, with a
+//          kernel to route it 19.6)
 //  kFew    few entries, from topk_ids
 //  kEntry  a workgroup per entry of topk_ids
 //  kExpert a workgroup per expert (more entries than experts)
@@ -326,7 +327,10 @@ __device__ __forceinline__ int many_entries(const MoeArgs& a, ManyEntries& m, in
 // the rows of W1 and those of W3 that belong to them, over all of `hidden`, its
 // waves taking contiguous runs of the steps.  16 NB entries at a time are the
 // matrix columns; columns past the last repeat it, and no result of theirs is
-// stored.
+// stored.  Bound by the weights' bytes, at what loads three or four waves of a
+// SIMD keep on their way: 394 MB in 86 us in FP4 (4.6 TB/s), 553 MB in 102 us
+// in E4M3 (5.4 TB/s).  More waves with fewer registers, steps loaded ahead in
+// each wave, or two or eight waves a workgroup were no faster.
 
 constexpr int kUpWaves = 4, kUpThreads = 64 * kUpWaves;
 
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int
                             xr[0] + min(c * S + 128 * i, a.hidden - 128) + 8 * s);
             }
             // all of the step's loads before any use: the compiler sank them past the first
-            // chunks' products (16 tokens over 256 experts, 7168 x 512: 113 us to 94)
+            // chunks' products (16 tokens over 256 experts, 7168 x 512: 153 us a call, 149 so)
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
 // is computed, the next one's h and the next steps' weights are on their way,
 // over the ends of experts too: a workgroup for each expert spent its life
 // waiting for its first loads (128 entries, 101 experts of 7168 x 512 in FP4:
-// 92 us, this form 56, of which the weights at 6.2 TB/s are 32).  The parts,
+// 92 us, this form 54, of which the weights at 6.2 TB/s are 32).  The parts,
 // times the tokens' weights, go to memory in 32 bits, a row an entry, and a
 // third kernel adds a token's rows in their order.
 
@@ -850,11 +854,11 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
     }
     // One block of 16 entries, whose waves are more at a time, unless experts commonly have more:
     // they would read their weights again.  64 tokens, 4096 x 1024 in E4M3: 4 of 64 experts (4 an
-    // expert) 172 us and 181 with two, 2 of 8 (16 an expert) 68 and 62.
+    // expert) 158 us and 167 with two, 2 of 8 (16 an expert) 60 and 56.
     const bool narrow = a.tokens <= 16 || entries <= 10 * a.experts;
     // Wide tiles (x read once for twice the weights) where they give workgroups enough: 16 tokens
-    // (1536 wide tiles, 2048 x 768) 71.8 us and 79.2 narrow, 4 (768) 35.5 and 38.2; but 1 token
-    // (128, 7168 x 512) 34.4 and 28.2.
+    // (1536 wide tiles, 2048 x 768) 68.5 us and 75.8 narrow, 4 (768) 33.5 and 35.3; but 1 token
+    // (128, 7168 x 512) 29.5 and 24.9.
     if (units * (a.inter / 32) >= 768) {
         if (narrow) launch_up<FMT, 1, 2>(a, few, routed, stream);
         else launch_up<FMT, 2, 2>(a, few, routed, stream);

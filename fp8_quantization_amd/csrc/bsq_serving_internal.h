@@ -132,8 +132,8 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTopk = 16;
 // Entries (a token's choices of an expert) that one wave's lanes hold, one block of matrix
 // columns: so few take the kernels without LDS tables and partial results, which save a launch
 // or two but whose down products have a workgroup for 16 columns only.  Both forms, with 8
-// experts a token of 128 (2048 x 768, FP4): 8 entries 18.5 and 27.2 us, 16 25.9 and 30.0, 24
-// 36.1 and 35.5, 32 44.3 and 38.2.
+// experts a token of 128 (2048 x 768, FP4): 8 entries 17.3 and 26.3 us, 16 23.7 and 28.5, 24
+// 32.6 and 31.7, 32 37.9 and 33.1.
 constexpr int kFewEntries = 16;
 inline bool moe_is_few(int64_t tokens, int64_t topk) { return tokens * topk <= kFewEntries; }
 hipError_t launch_moe(int fmt, const MoeArgs& a, hipStream_t stream);
