@@ -957,10 +957,10 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
 
 // How work is split, with 32 heads of 128 on 8.  Target: 64 sequences of 8192 tokens 115 us a
 // call (1024: 128, 4096: 114).  Least: 4 of 6000 tokens 14.3 us (8: 18.1, 32: 16.8).  None:
-// 16 sequences of 5 rows in a window of 1024, 8 heads of 64, 8.4 us (split 12.8).  kRowsLeast
-// and kRowsTarget: 100 rows of 8 heads in 6000 tokens 25 us (16 pages at least: 35).
+// 16 sequences of 5 rows in a window of 1024, 8 heads of 64, 8.4 us (split 12.8).  kRowsLeast:
+// 128 rows in 1024 tokens 18.8 us (8 pages at least: 23.8, 16: 29.8).
 constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40;
-constexpr int64_t kRowsLeast = 8, kRowsTarget = 512, kRowsFull = 128;
+constexpr int64_t kRowsLeast = 4;
 
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window) {
@@ -976,22 +976,25 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
         if (p.wide) p.block_cols = kWideColumns;
     }
     p.col_blocks = (int32_t)((cols + p.block_cols - 1) / p.block_cols);
-    // Runs of pages: as many as give `target` workgroups if every sequence were the longest, of
-    // `least` pages at least.  Joining costs a second kernel (4 us and more), as much as a
-    // workgroup of the split form takes for 32 pages more: up to kSplitNone it splits nothing.
-    // The rows form, which has more sums to join, splits where it leaves half the CUs without a
-    // workgroup: 100 rows of 8 heads in 6000 tokens 25 us, unsplit 144; 2 x 500 rows of 16 heads
-    // of 64 in 3000 tokens (128 workgroups) 40 and 55; but 256 workgroups 151 and 123.
+    // Joining costs a second kernel (4 us and more), as much as a workgroup of the split form
+    // takes for 32 pages more: up to kSplitNone pages that form splits nothing.
     const double blocks = heads * p.col_blocks;
-    const double target = p.rows_form ? kRowsTarget : kSplitTarget;
-    const int64_t least = p.rows_form ? kRowsLeast : kSplitLeast;
-    int64_t run = (int64_t)std::ceil(std::min((double)pages, (double)pages * blocks / target));
-    if (run < least) run = least;
-    if (p.rows_form) {
-        if (blocks > kRowsFull) run = pages + 1;
-    } else {
-        run = (run + kWaves - 1) / kWaves * kWaves;
+    int64_t run;
+    if (!p.rows_form) {
+        // runs that give kSplitTarget workgroups if every sequence were the longest
+        run = (int64_t)std::ceil(std::min((double)pages, (double)pages * blocks / kSplitTarget));
+        run = (std::max(run, kSplitLeast) + kWaves - 1) / kWaves * kWaves;
         if (pages <= kSplitNone) run = kSplitNone;
+    } else {
+        // The rows form splits until the CUs hold all the workgroups they can (3, 2 and 1 each by
+        // head_dim), but not where half of those are there already, nor where the pages are too
+        // few for the sums that are joined, which grow with the workgroups: 192 of 128 pages 153
+        // us, unsplit 187; 128 of 24 pages 37 and 42, of 16 32 and 31; 128 of 10 pages of
+        // head_dim 64 27 and 17; 8 of 94 pages 23 and 144.
+        const double slots = head_dim == 64 ? 768 : head_dim == 128 ? 512 : 256;
+        const bool many = blocks <= slots / 2 && blocks <= 256 && 16.0 * pages >= 3.0 * blocks;
+        const int64_t n = many && blocks > 0 ? std::llround(slots / blocks) : 1;
+        run = std::max((pages + n - 1) / n, kRowsLeast);
     }
     const int64_t splits = (pages + run - 1) / run;
     p.splits = splits < 1 ? 1 : (int32_t)splits;
