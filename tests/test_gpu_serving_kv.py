@@ -130,8 +130,9 @@ def test_append_skips_what_it_cannot_place(bsq):
 # ------------------------------------------------------------------ attention
 
 
-def attend(bsq, c, q, offsets, lens, table, scale, window=0, max_kv=None, dev=None, **kw):
-    n = int(np.max(np.diff(np.asarray(offsets)), initial=0))
+def attend(bsq, c, q, offsets, lens, table, scale, window=0, max_kv=None, dev=None, max_q=None,
+           **kw):
+    n = max_q or int(np.max(np.diff(np.asarray(offsets)), initial=0))
     return bsq.kv_cache_attention(dev_rows(q), dev or dev_cache(bsq, c), i32(offsets), i32(lens),
                                   i32(table), n, int(max(lens)) if max_kv is None else max_kv,
                                   scale=scale, window=window, return_lse=True, **kw)
@@ -228,6 +229,19 @@ def test_split_over_the_tokens(bsq, rows, kv):
     check(bsq, c, q, off, lens, table, D ** -0.5, max_kv=70000)
     check(bsq, c, q, off, lens, table, D ** -0.5, max_kv=1)
     check(bsq, c, q, off, lens, table, D ** -0.5, window=2777)
+
+
+@pytest.mark.parametrize("hq,heads", [(2, 2), (7, 1), (6, 2)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_many_rows_in_wide_workgroups(bsq, hq, heads, window):
+    """head_dim 128 takes 256 columns a workgroup where a call may have 512 of them: so does a
+    loose bound on the rows.  NaN scales there as well."""
+    rows, lens = [300, 1, 0, 257], [300, 200, 70, 501]
+    c, q, off, table = make(hq, lens, rows, heads, hq, 128)
+    check(bsq, c, q, off, lens, table, 128 ** -0.5, window, max_q=512 * 256 // heads)
+    c.ks[table[0][4], 0] = 255
+    c.vs[table[3][7], heads - 1] = 255
+    check(bsq, c, q, off, lens, table, 128 ** -0.5, window, max_q=512 * 256 // heads)
 
 
 def test_more_than_64_splits(bsq):
