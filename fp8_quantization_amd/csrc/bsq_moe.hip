@@ -833,14 +833,17 @@ void launch_up(const MoeArgs& a, bool few, bool routed, hipStream_t stream) {
     const int tiles = a.inter / (16 * G), entries = a.tokens * a.topk;
     const dim3 by_entry((uint32_t)(entries * tiles)), by_expert((uint32_t)(a.experts * tiles));
     const dim3 block(kUpThreads);
-    if (few && !routed)
-        hipLaunchKernelGGL((moe_up_kernel<FMT, NB, G, kRoute>), by_entry, block, 0, stream, a, tiles);
-    else if (few)
-        hipLaunchKernelGGL((moe_up_kernel<FMT, NB, G, kFew>), by_entry, block, 0, stream, a, tiles);
-    else if (entries <= a.experts)
-        hipLaunchKernelGGL((moe_up_kernel<FMT, NB, G, kEntry>), by_entry, block, 0, stream, a, tiles);
-    else
+    // two blocks of entries: more entries than experts by far
+    if (NB == 2 || (!few && entries > a.experts)) {
         hipLaunchKernelGGL((moe_up_kernel<FMT, NB, G, kExpert>), by_expert, block, 0, stream, a, tiles);
+    } else if constexpr (NB == 1) {
+        if (few && !routed)
+            hipLaunchKernelGGL((moe_up_kernel<FMT, 1, G, kRoute>), by_entry, block, 0, stream, a, tiles);
+        else if (few)
+            hipLaunchKernelGGL((moe_up_kernel<FMT, 1, G, kFew>), by_entry, block, 0, stream, a, tiles);
+        else
+            hipLaunchKernelGGL((moe_up_kernel<FMT, 1, G, kEntry>), by_entry, block, 0, stream, a, tiles);
+    }
 }
 
 template <int FMT>

@@ -79,6 +79,27 @@ def test_routed_by_the_caller(bsq, fmt, T, E, k, H, I):  # noqa: F811
     assert torch.equal(i2.cpu(), torch.from_numpy(ids)) and torch.equal(w2.cpu(), torch.from_numpy(w))
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (2, 20, 8, 128, 1664), (8, 16, 2, 640, 1536), (16, 200, 8, 128, 256), (64, 100, 2, 384, 256),
+    (64, 24, 12, 128, 1024)])
+def test_wide_tiles(bsq, fmt, T, E, k, H, I):  # noqa: F811
+    """Columns of h enough for 32 a workgroup: few entries, a workgroup an entry or an expert, one
+    block of entries and two."""
+    L = Layer(T + E, E, H, I, fmt)
+    x = R.bf16(np.random.default_rng(T).standard_normal((T, H)))
+    ids, w = given(T * E, T, E, k)
+    y, _, _ = bsq.moe_few_tokens(dev_rows(x), fmt, *L.dev(), E, k, topk_ids=i32(ids),
+                                 topk_weights=torch.from_numpy(w).cuda())
+    torch.cuda.synchronize()
+    check(y, *L.reference(x, ids, w))
+    logits = np.random.default_rng(E).standard_normal((T, E)).astype(np.float32)
+    y, i2, w2 = bsq.moe_few_tokens(dev_rows(x), fmt, *L.dev(), E, k,
+                                   router_logits=torch.from_numpy(logits).cuda())
+    torch.cuda.synchronize()
+    check(y, *L.reference(x, i2.cpu().numpy(), w2.cpu().numpy()))
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 @pytest.mark.parametrize("T,E,k", [(1, 8, 2), (2, 128, 8), (4, 129, 16), (5, 256, 8), (3, 1024, 5),
                                    (20, 65, 1), (64, 16, 4)])
