@@ -9,7 +9,7 @@
 // one of a wrong size BsqError (the class handed to `init`), before anything
 // runs.
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
-#include <c10/hip/HIPCachingAllocator.h>
+#include <c10/core/StreamGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/torch.h>
 
@@ -84,24 +84,46 @@ struct Args {
         return &t;
     }
     std::optional<at::Device> device;
-    bool other_stream = false;
+};
 
-    // The stream (an object with cuda_stream, or None for the current one).
-    void* stream() {
-        PyObject* o = next();
-        if (o == Py_None)
-            return at::hip::getCurrentHIPStreamMasqueradingAsCUDA(device->index()).stream();
-        other_stream = true;
-        PyObject* raw = PyObject_GetAttrString(o, "cuda_stream");
-        if (!raw) {
+// The stream of a call (an object with cuda_stream, or None for the current one).  It is torch's
+// current stream as long as this lives, so whatever the call allocates belongs to it: its memory
+// has been used by earlier work of that stream alone, and goes to later work of it alone.  With
+// memory of the caller's stream the kernels could overwrite what that stream is still reading.
+struct CallStream {
+    void* raw;
+    explicit CallStream(Args& a) {
+        PyObject* o = a.next();
+        const auto now = at::hip::getCurrentHIPStreamMasqueradingAsCUDA(a.device->index());
+        raw = now.stream();
+        if (o == Py_None) return;
+        PyObject* attr = PyObject_GetAttrString(o, "cuda_stream");
+        if (!attr) {
             PyErr_Clear();
             refuse(0, "stream must be a torch.cuda.Stream");
         }
-        void* s = PyLong_AsVoidPtr(raw);
-        Py_DECREF(raw);
-        if (!s && PyErr_Occurred()) PyErr_Clear();
-        return s;
+        void* given = PyLong_AsVoidPtr(attr);
+        Py_DECREF(attr);
+        if (!given && PyErr_Occurred()) {
+            PyErr_Clear();
+            refuse(0, "stream must be a torch.cuda.Stream");
+        }
+        if (given == raw) return;
+        raw = given;
+        caller = now.unwrap();
+        guard.reset_stream(at::hip::getStreamFromExternalMasqueradingAsCUDA(
+            static_cast<hipStream_t>(given), a.device->index()).unwrap());
     }
+    // An output for the caller; one that the call allocated itself (`own`) will be used by the
+    // caller's stream too, so its memory must not go to this one's work before that is done.
+    PyObject* give(const at::Tensor& t, const at::Tensor& own) const {
+        if (caller && own.defined()) own.record_stream(*caller);
+        return THPVariable_Wrap(t);
+    }
+
+private:
+    std::optional<c10::Stream> caller;   // the caller's stream, where it is another
+    c10::OptionalStreamGuard guard;
 };
 
 // Whether the dimensions after the first lie without gaps.
@@ -211,13 +233,13 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const at::Device& 
     return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
 }
 
-// Workspace of a call: the caller's, or an allocation whose memory is not given to
-// another stream's work before the call's stream is past it.
+// Workspace of a call: the caller's, or an allocation that the call's stream owns (a CallStream
+// lives), given back at the call's end to later work of that stream.
 struct Workspace {
     at::Tensor own;
     void* p = nullptr;
     int64_t bytes = 0;
-    Workspace(Args& a, const at::Tensor* given, int64_t need, void* stream) {
+    Workspace(Args& a, const at::Tensor* given, int64_t need) {
         if (given) {
             if (given->scalar_type() != at::kByte || !given->is_contiguous())
                 refuse(0, "workspace must be a contiguous uint8 GPU tensor");
@@ -225,9 +247,6 @@ struct Workspace {
             bytes = given->numel();
         } else if (need > 0) {
             own = empty({need}, at::kByte, *a.device);
-            if (a.other_stream)
-                own.record_stream(at::hip::getStreamFromExternalMasqueradingAsCUDA(
-                    static_cast<hipStream_t>(stream), a.device->index()).unwrap());
             p = own.data_ptr();
             bytes = need;
         }
@@ -269,7 +288,7 @@ PyObject* append(Args& a) {
     const at::Tensor* offsets = a.tensor("row_offsets");
     const Table t = table_of(a);
     const int64_t max_new = a.integer("max_new");
-    void* stream = a.stream();
+    const CallStream stream(a);
     vec(offsets, "row_offsets", at::kUInt32, t.seqs + 1, true);
     for (const at::Tensor* x : {&k, &v})
         if (x->size(1) != c.num_heads || x->size(2) != c.head_dim || x->size(0) != k.size(0))
@@ -277,7 +296,7 @@ PyObject* append(Args& a) {
                    c.num_heads, c.head_dim);
     check(kv_cache_append(&c, k.data_ptr(), row_stride(k), v.data_ptr(), row_stride(v),
                           static_cast<uint32_t*>(offsets->data_ptr()), t.lens, t.p, t.stride, t.pages,
-                          t.seqs, k.size(0), max_new, stream));
+                          t.seqs, k.size(0), max_new, stream.raw));
     return none();
 }
 
@@ -295,7 +314,7 @@ PyObject* attention(Args& a) {
     const at::Tensor* lse = a.tensor("lse", true);
     const bool want_lse = a.integer("return_lse") != 0;
     const at::Tensor* given = a.tensor("workspace", true);
-    void* stream = a.stream();
+    const CallStream stream(a);
     const int64_t R = q.size(0), Hq = q.size(1), D = q.size(2);
     if (D != c.head_dim)
         refuse(BSQ_ERR_INVALID_ARG, "q is %lld wide, the cache's heads %d", (long long)D, c.head_dim);
@@ -318,15 +337,15 @@ PyObject* attention(Args& a) {
     }
     const int64_t need = size_of(kv_cache_attention_workspace(c.num_heads, D, Hq, t.seqs, R, max_q,
                                                               max_kv, window));
-    const Workspace ws(a, need ? given : nullptr, need, stream);
+    const Workspace ws(a, need ? given : nullptr, need);
     check(kv_cache_attention(&c, q.data_ptr(), row_stride(q), Hq,
                              static_cast<uint32_t*>(offsets->data_ptr()), t.lens, t.p, t.stride,
                              t.pages, t.seqs, R, max_q, max_kv, (float)scale, window,
                              out->data_ptr(), row_stride(*out),
                              lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.p, ws.bytes,
-                             stream));
-    PyObject* o = THPVariable_Wrap(*out);
-    PyObject* l = lse ? THPVariable_Wrap(*lse) : none();
+                             stream.raw));
+    PyObject* o = stream.give(*out, new_out);
+    PyObject* l = lse ? stream.give(*lse, new_lse) : none();
     PyObject* r = o && l ? PyTuple_Pack(2, o, l) : nullptr;
     Py_XDECREF(o);
     Py_XDECREF(l);
@@ -340,7 +359,8 @@ PyObject* pages_copy(Args& a) {
     const int64_t n = src->numel();
     const int32_t* s = vec(src, "src", at::kInt, n, true).data_ptr<int32_t>();
     const int32_t* d = vec(a.tensor("dst"), "dst", at::kInt, n, true).data_ptr<int32_t>();
-    check(kv_pages_copy(&c, s, d, n, a.stream()));
+    const CallStream stream(a);
+    check(kv_pages_copy(&c, s, d, n, stream.raw));
     return none();
 }
 
@@ -361,12 +381,14 @@ PyObject* pages_reserve(Args& a) {
     const int64_t n = slots->numel();
     vec(slots, "slots", at::kInt, n, true);
     const at::Tensor& add = vec(a.tensor("add_tokens"), "add_tokens", at::kInt, n, true);
+    const at::Tensor* given = a.tensor("status", true);
+    const CallStream stream(a);
     at::Tensor own;
-    const at::Tensor* status = status_of(a.tensor("status", true), n, own, a);
+    const at::Tensor* status = status_of(given, n, own, a);
     check(kv_pages_reserve(t.p, t.stride, t.pages, t.seqs, t.lens, refs.data_ptr<int32_t>(),
                            refs.numel(), slots->data_ptr<int32_t>(), add.data_ptr<int32_t>(), n,
-                           status->data_ptr<int32_t>(), a.stream()));
-    return THPVariable_Wrap(*status);
+                           status->data_ptr<int32_t>(), stream.raw));
+    return stream.give(*status, own);
 }
 
 // cache, block_table, kv_lens, refcounts, parents, children, status, stream -> status
@@ -378,12 +400,14 @@ PyObject* pages_fork(Args& a) {
     const int64_t n = parents->numel();
     vec(parents, "parents", at::kInt, n, true);
     const at::Tensor& children = vec(a.tensor("children"), "children", at::kInt, n, true);
+    const at::Tensor* given = a.tensor("status", true);
+    const CallStream stream(a);
     at::Tensor own;
-    const at::Tensor* status = status_of(a.tensor("status", true), n, own, a);
+    const at::Tensor* status = status_of(given, n, own, a);
     check(kv_pages_fork(&c, t.p, t.stride, t.pages, t.seqs, t.lens, refs.data_ptr<int32_t>(),
                         parents->data_ptr<int32_t>(), children.data_ptr<int32_t>(), n,
-                        status->data_ptr<int32_t>(), a.stream()));
-    return THPVariable_Wrap(*status);
+                        status->data_ptr<int32_t>(), stream.raw));
+    return stream.give(*status, own);
 }
 
 // block_table, kv_lens, refcounts, slots, stream
@@ -391,8 +415,9 @@ PyObject* pages_free(Args& a) {
     const Table t = table_of(a);
     const at::Tensor& refs = vec(a.tensor("refcounts"), "refcounts", at::kInt, 0, false);
     const at::Tensor& slots = vec(a.tensor("slots"), "slots", at::kInt, 0, false);
+    const CallStream stream(a);
     check(kv_pages_free(t.p, t.stride, t.pages, t.seqs, t.lens, refs.data_ptr<int32_t>(), refs.numel(),
-                        slots.data_ptr<int32_t>(), slots.numel(), a.stream()));
+                        slots.data_ptr<int32_t>(), slots.numel(), stream.raw));
     return none();
 }
 
@@ -406,7 +431,7 @@ PyObject* pages_compact(Args& a) {
     const at::Tensor* counts = a.tensor("refcounts_out", true);
     const at::Tensor* live = a.tensor("num_live", true);
     const at::Tensor* given = a.tensor("workspace", true);
-    void* stream = a.stream();
+    const CallStream stream(a);
     at::Tensor new_table, new_counts, new_live;
     if (!table) {
         new_table = empty({t.seqs, t.pages}, at::kInt, *a.device);
@@ -427,11 +452,12 @@ PyObject* pages_compact(Args& a) {
         live = &new_live;
     }
     vec(live, "num_live", at::kInt, 1, false);
-    const Workspace ws(a, given, size_of(kv_pages_compact_workspace(c.num_pages)), stream);
+    const Workspace ws(a, given, size_of(kv_pages_compact_workspace(c.num_pages)));
     check(kv_pages_compact(&c, t.p, t.stride, t.pages, t.seqs, t.lens, refs.data_ptr<int32_t>(), rows,
                            stride, counts->data_ptr<int32_t>(), live->data_ptr<int32_t>(), ws.p,
-                           ws.bytes, stream));
-    PyObject* o[3] = {THPVariable_Wrap(*table), THPVariable_Wrap(*counts), THPVariable_Wrap(*live)};
+                           ws.bytes, stream.raw));
+    PyObject* o[3] = {stream.give(*table, new_table), stream.give(*counts, new_counts),
+                      stream.give(*live, new_live)};
     PyObject* r = o[0] && o[1] && o[2] ? PyTuple_Pack(3, o[0], o[1], o[2]) : nullptr;
     for (PyObject* x : o) Py_XDECREF(x);
     return r;
@@ -455,7 +481,7 @@ PyObject* moe(Args& a) {
     const int64_t renormalize = a.integer("renormalize");
     const at::Tensor* out = a.tensor("out", true);
     const at::Tensor* given = a.tensor("workspace", true);
-    void* stream = a.stream();
+    const CallStream stream(a);
     const int64_t T = x.size(0), H = x.size(1);
     if (w13->dim() != 2 || E < 1 || w13->size(0) % (2 * E) != 0)
         refuse(BSQ_ERR_INVALID_ARG,
@@ -497,13 +523,14 @@ PyObject* moe(Args& a) {
     matrix(weights, "topk_weights", at::kFloat, T, k);
     // sizes that the workspace refuses are refused by the call, with its message
     const int64_t need = moe_few_tokens_workspace(T, H, I, k);
-    const Workspace ws(a, given, need < 0 ? 0 : need, stream);
+    const Workspace ws(a, given, need < 0 ? 0 : need);
     check(moe_few_tokens(fmt, x.data_ptr(), row_stride(x), T, H, I, E, k, w13->data_ptr(),
                          w13s->data_ptr(), w2->data_ptr(), w2s->data_ptr(),
                          logits ? logits->data_ptr<float>() : nullptr, (int)renormalize,
                          ids->data_ptr<int32_t>(), weights->data_ptr<float>(), out->data_ptr(),
-                         row_stride(*out), ws.p, ws.bytes, stream));
-    PyObject* o[3] = {THPVariable_Wrap(*out), THPVariable_Wrap(*ids), THPVariable_Wrap(*weights)};
+                         row_stride(*out), ws.p, ws.bytes, stream.raw));
+    PyObject* o[3] = {stream.give(*out, new_out), stream.give(*ids, new_ids),
+                      stream.give(*weights, new_weights)};
     PyObject* r = o[0] && o[1] && o[2] ? PyTuple_Pack(3, o[0], o[1], o[2]) : nullptr;
     for (PyObject* p : o) Py_XDECREF(p);
     return r;

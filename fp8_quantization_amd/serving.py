@@ -7,7 +7,10 @@ these for a few microseconds of GPU work each, so the checks and the launch
 are in a native module (``csrc/bsq_serving_py.cpp``): through ctypes, checking
 eight to ten tensors took 18 to 30 us a call.  A size that does not fit raises
 ``BsqError``, a wrong dtype, device or layout ``TypeError``, before anything
-runs.  Kernels run on ``stream``, or on torch's current stream.
+runs.  Kernels run on ``stream``, or on torch's current stream.  With another
+stream than the current one, as in torch: the inputs must be ready on it (and
+stay until it has read them), the results are ready once the current stream
+waits for it; outputs and workspaces that a call allocates are that stream's.
 """
 import ctypes
 import os
