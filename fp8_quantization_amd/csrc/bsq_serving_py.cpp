@@ -9,6 +9,7 @@
 // one of a wrong size BsqError (the class handed to `init`), before anything
 // runs.
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/torch.h>
@@ -90,10 +91,13 @@ struct Args {
 // current stream as long as this lives, so whatever the call allocates belongs to it: its memory
 // has been used by earlier work of that stream alone, and goes to later work of it alone.  With
 // memory of the caller's stream the kernels could overwrite what that stream is still reading.
+// The tensors' device is the current one meanwhile: launched with another current, kernels on a
+// device's default stream would run on that other one.
 struct CallStream {
     void* raw;
     explicit CallStream(Args& a) {
         PyObject* o = a.next();
+        device.reset_device(*a.device);
         const auto now = at::hip::getCurrentHIPStreamMasqueradingAsCUDA(a.device->index());
         raw = now.stream();
         if (o == Py_None) return;
@@ -123,6 +127,7 @@ struct CallStream {
 
 private:
     std::optional<c10::Stream> caller;   // the caller's stream, where it is another
+    c10::OptionalDeviceGuard device;
     c10::OptionalStreamGuard guard;
 };
 

@@ -169,3 +169,26 @@ def test_another_stream_in_a_captured_graph(bsq):  # noqa: F811
         assert c.right(got)
         assert c.right(c.call(torch.cuda.current_stream()))
         torch.cuda.synchronize()
+
+
+def test_current_stream_and_device_after_a_call(bsq):  # noqa: F811
+    """A call on another stream, and one that is refused there, leave the current one current."""
+    c, side, now = Call(bsq, "attention"), torch.cuda.Stream(), torch.cuda.current_stream()
+    c.call(side)
+    assert torch.cuda.current_stream() == now
+    d, q = bsq.kv_cache(3, 1, 64), torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(bsq.BsqError):
+        bsq.kv_cache_attention(q, d, i32([0, 1]), i32([0]), i32([[0]]), 1, 1, window=-1, stream=side)
+    assert torch.cuda.current_stream() == now and torch.cuda.current_device() == 0
+    torch.cuda.synchronize()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_tensors_of_another_device(bsq):  # noqa: F811
+    """Tensors of a device that is not the current one: the call runs there."""
+    with torch.cuda.device(1):
+        c = Call(bsq, "attention")
+    now = torch.cuda.current_device()
+    got = c.call(None)
+    torch.cuda.synchronize(1)
+    assert now == torch.cuda.current_device() and got[0].device.index == 1 and c.right(got)
