@@ -316,11 +316,13 @@ struct Columns {
 // V's scale goes into its conversion to FP16, relative to acc's unit: exact
 // within [-15, 7] of it.  Past that the unit moves, but stays within 2^60 of the
 // largest scale so far: acc, at most 2^9 2^15 2^60 a token, then cannot overflow.
-__device__ __forceinline__ int v_exponent(uint32_t vs) { return vs == 255u ? 0 : (int)vs - 127; }
+// A page with the NaN scale moves neither: its codes enter as they are, beside weights that are
+// NaN where a row sees it and 0 where none does.
 struct Unit {
     int unit = -1000, top = -1000;   // of acc; the largest scale so far
     __device__ __forceinline__ void follow(uint32_t vs) {
-        const int e = v_exponent(vs);
+        if (vs == 255u) return;
+        const int e = (int)vs - 127;
         top = max(top, e);
         if (e > unit + 7 || e < unit - 15) unit = max(e, top - 60);
     }
@@ -330,7 +332,7 @@ __device__ __forceinline__ float power_of_two(int n) {
     return n < -126 ? 0.0f : __uint_as_float((uint32_t)(min(n, 127) + 127) << 23);
 }
 __device__ __forceinline__ float v_factor(uint32_t vs, int unit) {
-    return power_of_two(v_exponent(vs) - unit);
+    return vs == 255u ? 1.0f : power_of_two((int)vs - 127 - unit);
 }
 // Of the dword of V that holds tokens t .. t + 3, the bytes before the
 // sequence's end: those past it may hold anything.
