@@ -333,6 +333,7 @@ __device__ __forceinline__ int many_entries(const MoeArgs& a, ManyEntries& m, in
 // each wave, or two or eight waves a workgroup were no faster.
 
 constexpr int kUpWaves = 4, kUpThreads = 64 * kUpWaves;
+constexpr float kBf16Max = 0x1.FEp127f;
 
 template <int FMT, int NB, int G, RowsFrom FROM>
 __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int tiles) {
@@ -464,13 +465,15 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(const MoeArgs a, int
                 up += part[k][G + wave][lane];
             }
             // h as the sum of two BF16 numbers, 16 bits in all: with one, its rounding
-            // alone made y's error 1.4 to 1.5 times that of rounding y
+            // alone made y's error 1.4 to 1.5 times that of rounding y.  The first stays
+            // finite, so that the second is never the difference of two infinities: it
+            // holds what fp32 has past BF16's range, an infinity or a NaN.
             bf16x2 hi[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float h =
                     gate[e] / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * gate[e])) * up[e];
-                hi[e / 2][e % 2] = (__bf16)h;
+                hi[e / 2][e % 2] = (__bf16)fminf(fmaxf(h, -kBf16Max), kBf16Max);
                 lo[e / 2][e % 2] = (__bf16)(h - (float)hi[e / 2][e % 2]);
             }
             uint16_t* dst = a.h + (int64_t)row[b] * 2 * a.inter + 16 * (G * tile + wave) + 4 * g;
