@@ -76,9 +76,10 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs a) 
     if (sq.n == 0 || old < 0) return;
     const int64_t page_i = old / kKvPage + pi;
     const int64_t base = page_i * kKvPage;
-    if (base >= sq.L || page_i >= a.seqs.max_pages) return;
+    const int64_t end = min((int64_t)sq.L, old + a.max_new);   // of the rows that are written
+    if (base >= end || page_i >= a.seqs.max_pages) return;
     const int t0 = (int)(base < old ? old - base : 0);                   // first new token
-    const int t1 = (int)(sq.L - base < kKvPage ? sq.L - base : kKvPage);  // end of them
+    const int t1 = (int)(end - base < kKvPage ? end - base : kKvPage);   // end of them
     const int32_t page = a.seqs.table[(int64_t)s * a.seqs.table_stride + page_i];
     const int64_t ldx = a.ldx[is_v];
     const uint16_t* x = a.x[is_v] + (sq.lo + (base - old)) * ldx + (int64_t)head * D;
@@ -460,6 +461,10 @@ __device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<C
         }
 }
 
+// Columns of a sequence (its rows past max_q have none); with a block's more they fit an int.
+__device__ __forceinline__ int columns(const AttendArgs& a, const Seq& sq) {
+    return min(sq.n, a.max_q) * a.group;
+}
 // Column c of a sequence: its row (i), head of the group and the tokens it sees.
 struct Column {
     int i, head, first, last;
@@ -568,7 +573,7 @@ attend_split_kernel(const AttendArgs a) {
     b /= (uint32_t)a.col_blocks;
     const int split = (int)(b % (uint32_t)a.splits), s = (int)(b / (uint32_t)a.splits);
     const Seq sq = load_seq(a.seqs, s);
-    const int cols = (int)min((int64_t)sq.n * a.group, (int64_t)0x7FFFFFF0), c0 = 16 * blk;
+    const int cols = columns(a, sq), c0 = 16 * blk;
     if (c0 >= cols) return;
     const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -687,7 +692,7 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
     b /= (uint32_t)a.col_blocks;
     const int split = (int)(b % (uint32_t)a.splits), s = (int)(b / (uint32_t)a.splits);
     const Seq sq = load_seq(a.seqs, s);
-    const int cols = (int)min((int64_t)sq.n * a.group, (int64_t)0x7FFFFFF0);
+    const int cols = columns(a, sq);
     const int tid = (int)threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int w0 = 16 * CB * W * blk;              // the workgroup's first column
@@ -819,7 +824,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
     // splits past the sequence's pages hold nothing and are not read
     const int c0 = (i * a.group + head % a.group) / a.block_cols * a.block_cols;
     int p0, p1;
-    page_range(a, sq, c0, (int)min((int64_t)c0 + a.block_cols, (int64_t)sq.n * a.group) - 1, p0, p1);
+    page_range(a, sq, c0, min(c0 + a.block_cols, columns(a, sq)) - 1, p0, p1);
     const int used = (int)min((int64_t)a.splits,
                               ((int64_t)p1 - p0 + a.split_pages - 1) / a.split_pages);
     const int64_t row = sq.lo + i, at = row * a.num_q_heads + head;

@@ -131,7 +131,7 @@ int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_s
                     "num_seqs=%lld, max_q=%lld and max_kv=%lld must be in 0 .. 2^31 - 1, window=%lld "
                     ">= 0", (long long)num_seqs, (long long)max_q, (long long)max_kv,
                     (long long)window);
-    if (max_q * (num_q_heads / num_heads) > 0x7FFFFFF0LL)
+    if (max_q * (num_q_heads / num_heads) > 0x7FFFFE00LL)
         return fail(BSQ_ERR_INVALID_ARG, "max_q=%lld rows of %lld heads are too many",
                     (long long)max_q, (long long)num_q_heads);
     if (num_seqs == 0 || max_q == 0) {

@@ -1,11 +1,12 @@
 """Edges of the serving operators: pages without a number in their scale beside far smaller ones,
-numbers at the ends of their range."""
+numbers at the ends of their range, rows past the host-side bounds."""
 import numpy as np
 import pytest
 import torch
 
 import serving_ref as R
-from test_gpu_serving_kv import bsq, check, dev_rows, i32, make  # noqa: F401
+from test_gpu_serving_kv import (attend, bsq, check, deal, dev_cache, dev_rows, i32,  # noqa: F401
+                                 make, random_cache, same_cache)
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,48 @@ def test_hidden_values_past_the_bf16_range(bsq, T):  # noqa: F811
     y = run()
     torch.cuda.synchronize()
     assert torch.all(y == np.inf)
+
+
+# ------------------------------------------------------------------ host-side bounds
+
+
+@pytest.mark.parametrize("most", [1, 2, 5, 6, 40, 64, 70])
+def test_append_stops_at_its_bound(bsq, most):  # noqa: F811
+    """Rows of a sequence past max_new are not written and have no part in a scale."""
+    rng = np.random.default_rng(most)
+    heads, D, olds, news = 2, 64, [0, 3, 62, 130, 64], [1, 9, 7, 200, 64]
+    lens = [a + b for a, b in zip(olds, news)]
+    pages, width = sum(R.pages_of(n) for n in lens) + 2, max(R.pages_of(n) for n in lens)
+    c = random_cache(rng, pages, heads, D)
+    table = deal(rng, lens, pages, width)
+    off = np.concatenate([[0], np.cumsum(news)])
+    x = R.bf16(rng.standard_normal((off[-1], heads, D)) * 2.0 ** np.arange(off[-1] // 9 + 1).repeat(9)
+               [:off[-1], None, None] * 2.0 ** -20)
+    d = dev_cache(bsq, c)
+    bsq.kv_cache_append(d, dev_rows(x), dev_rows(-x), i32(off), i32(lens), i32(table), most)
+    for s, n in enumerate(news):
+        m = min(n, most)
+        rows = slice(off[s], off[s] + m)
+        R.append(c, x[rows], -x[rows], [0, m], [olds[s] + m], [table[s]])
+    torch.cuda.synchronize()
+    same_cache(d, c)
+
+
+@pytest.mark.parametrize("D,hq,heads", [(64, 4, 2), (128, 4, 2), (256, 2, 1)])
+@pytest.mark.parametrize("most,lens", [(1, [300, 70, 9]), (3, [300, 70, 9]), (2, [3000, 200, 9]),
+                                       (70, [400, 150, 9]), (100, [400, 150, 9]), (90, [4000, 150, 9]), (100, [200, 150, 9]), (3, [140, 70, 9])])
+def test_attention_stops_at_its_bound(bsq, D, hq, heads, most, lens):  # noqa: F811
+    """Rows of a sequence past max_q keep what out and lse held, and the others their places."""
+    rows = [130, 40, 5]
+    c, q, off, table = make(D + most, lens, rows, heads, hq, D)
+    out = torch.full((off[-1], hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((off[-1], hq), 5.0, device="cuda")
+    attend(bsq, c, q, off, lens, table, 0.1, max_q=most, out=out, lse=lse)
+    torch.cuda.synchronize()
+    want, wlse, bo, bl, _ = R.attention(c, q, off, lens, table, 0.1)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for s, n in enumerate(rows):
+        done, left = slice(off[s], off[s] + min(n, most)), slice(off[s] + min(n, most), off[s + 1])
+        assert np.all(np.abs(out[done] - want[done]) <= bo[done])
+        assert np.all(np.abs(lse[done] - wlse[done]) <= bl[done])
+        assert np.all(out[left] == 7) and np.all(lse[left] == 5), s
