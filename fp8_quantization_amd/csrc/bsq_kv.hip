@@ -314,27 +314,25 @@ struct Columns {
     int all_from, all_to;            // tokens that every column of the wave sees
 };
 
-// V's scale goes into its conversion to FP16, relative to acc's unit: exact
-// within [-15, 7] of it.  Past that the unit moves, but stays within 2^60 of the
-// largest scale so far: acc, at most 2^9 2^15 2^60 a token, then cannot overflow.
-// A page with the NaN scale moves neither: its codes enter as they are, beside weights that are
-// NaN where a row sees it and 0 where none does.
-struct Unit {
-    int unit = -1000, top = -1000;   // of acc; the largest scale so far
-    __device__ __forceinline__ void follow(uint32_t vs) {
-        if (vs == 255u) return;
-        const int e = (int)vs - 127;
-        top = max(top, e);
-        if (e > unit + 7 || e < unit - 15) unit = max(e, top - 60);
-    }
-};
 // 2^n for the n of units and scales; below the normal numbers 0.
 __device__ __forceinline__ float power_of_two(int n) {
     return n < -126 ? 0.0f : __uint_as_float((uint32_t)(min(n, 127) + 127) << 23);
 }
-__device__ __forceinline__ float v_factor(uint32_t vs, int unit) {
-    return vs == 255u ? 1.0f : power_of_two((int)vs - 127 - unit);
-}
+// V's scale goes into its conversion to FP16, relative to acc's unit: exact
+// within [-15, 7] of it.  Past that the unit moves, but stays within 2^60 of the
+// largest scale so far: acc, at most 2^9 2^15 2^60 a token, then cannot overflow.
+// A page with the NaN scale leaves the unit and enters in it, beside weights that
+// are NaN where a row sees it and 0 where none does.
+struct Unit {
+    int unit = -1000, top = -1000;   // of acc; the largest scale so far (never below the unit)
+    // The factor of V's conversion.
+    __device__ __forceinline__ float follow(uint32_t vs) {
+        const int e = vs == 255u ? unit : (int)vs - 127;
+        top = max(top, e);
+        if (e > unit + 7 || e < unit - 15) unit = max(e, top - 60);
+        return power_of_two(e - unit);
+    }
+};
 // Of the dword of V that holds tokens t .. t + 3, the bytes before the
 // sequence's end: those past it may hold anything.
 __device__ __forceinline__ uint32_t before_end(int t, int L) {
@@ -614,9 +612,8 @@ attend_split_kernel(const AttendArgs a) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) vr[i] = load(vb + i * 1024);
         const uint32_t ks = a.cache.k_scales[so_], vs = a.cache.v_scales[so_];
-        unit.follow(vs);
+        const float vf = unit.follow(vs);
         if (unit.unit != st.unit) move_unit(st, unit.unit);
-        const float vf = v_factor(vs, unit.unit);
         if (p * kKvPage + kKvPage > sq.L) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
@@ -749,8 +746,7 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
         if (page_in < 0) return;
         ks = __builtin_amdgcn_readfirstlane(ks_v);
         vs = __builtin_amdgcn_readfirstlane(vs_v);
-        unit.follow(vs);
-        const float vf = v_factor(vs, unit.unit);
+        const float vf = unit.follow(vs);
         if (p * kKvPage + kKvPage > sq.L) {
 #pragma unroll
             for (int k = 0; k < kLoads; ++k)
