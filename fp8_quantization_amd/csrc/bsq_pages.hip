@@ -21,21 +21,22 @@ constexpr int kCopyBytes = kCopyThreads * 16 * 4;
 __device__ __forceinline__ int pages_of(int tokens) { return (int)(((int64_t)tokens + kKvPage - 1) / kKvPage); }
 
 // Exclusive prefix sum over the workgroup's threads; total gets the sum.  `tmp` holds
-// kScanWaves + 1 ints, free again when the call returns.
-__device__ __forceinline__ int block_prefix(int v, int* tmp, int& total) {
+// kScanWaves numbers, free again when the call returns.
+template <typename T>
+__device__ __forceinline__ T block_prefix(T v, T* tmp, T& total) {
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    int x = v;
+    T x = v;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(x, off);
+        const T y = __shfl_up(x, off);
         if (lane >= off) x += y;
     }
     if (lane == 63) tmp[wave] = x;
     __syncthreads();
-    int before = 0, all = 0;
+    T before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kScanWaves; ++w) {
-        const int t = tmp[w];
+        const T t = tmp[w];
         before += w < wave ? t : 0;
         all += t;
     }
@@ -79,7 +80,8 @@ __device__ __forceinline__ Request request(const PageArgs& p, int i) {
 // A chain of dependent loads and barriers bounds it, not its bytes.
 template <bool FORK, bool SMALL>
 __global__ void __launch_bounds__(kScanThreads) give_out_kernel(const PageArgs p) {
-    __shared__ int tmp[kScanWaves + 1];
+    __shared__ int tmp[kScanWaves];
+    __shared__ int64_t needs[kScanWaves];
     __shared__ Request kept[SMALL ? kScanThreads : 1];
     __shared__ int ranks[SMALL ? kScanThreads : 1];
     const int tid = (int)threadIdx.x;
@@ -101,8 +103,9 @@ __global__ void __launch_bounds__(kScanThreads) give_out_kernel(const PageArgs p
         const int i = i0 + tid;
         Request r{0, 0, 0, 0};
         if (i < p.n) r = request<FORK>(p, i);
-        int total;
-        const int before = block_prefix(r.pages, tmp, total);
+        // in 64 bits: a step's requests may name 2^10 times 2^25 pages
+        int64_t total;
+        const int64_t before = block_prefix((int64_t)r.pages, needs, total);
         // ranks past every page stay past every page
         const int rank = (int)min(need + before, (int64_t)0x7FFFFFFF);
         if (SMALL) {
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_free_kernel(const PageArgs
 // (n), list those at n and above and the free ones below n, both in order
 // (there are as many), and pair them.
 __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const CompactArgs p) {
-    __shared__ int tmp[kScanWaves + 1];
+    __shared__ int tmp[kScanWaves];
     const int tid = (int)threadIdx.x, N = p.cache.num_pages;
     // the first kKept steps' counts stay in registers
     constexpr int kKept = 4;

@@ -1,5 +1,6 @@
 """Edges of the serving operators: pages without a number in their scale beside far smaller ones,
-numbers at the ends of their range, rows past the host-side bounds."""
+numbers at the ends of their range, rows past the host-side bounds,
+more pages asked for than there are numbers."""
 import numpy as np
 import pytest
 import torch
@@ -114,3 +115,24 @@ def test_attention_stops_at_its_bound(bsq, D, hq, heads, most, lens):  # noqa: F
         assert np.all(np.abs(out[done] - want[done]) <= bo[done])
         assert np.all(np.abs(lse[done] - wlse[done]) <= bl[done])
         assert np.all(out[left] == 7) and np.all(lse[left] == 5), s
+
+
+# ------------------------------------------------------------------ pages
+
+
+@pytest.mark.parametrize("n,width", [(70, 2 ** 25 - 1), (1030, 2 ** 21)])
+def test_needs_past_32_bits(bsq, n, width):  # noqa: F811
+    """Requests whose needs add up to more than 2^31 pages: those that were served before the pages
+    ended have them, the others fail and change neither lengths nor counts."""
+    pages = 40
+    table = torch.empty((n, width), dtype=torch.int32, device="cuda")      # 9 GB, hardly touched
+    lens = torch.zeros(n, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    add = [64 * width if width < 2 ** 25 else 2 ** 31 - 64] * n
+    add[0], add[1], add[-1] = 130, 1, 64
+    status = bsq.kv_pages_reserve(table, lens, refs, i32(np.arange(n)), i32(add))
+    torch.cuda.synchronize()
+    assert status.tolist() == [0, 0] + [1] * (n - 2)
+    assert lens.tolist() == [130, 1] + [0] * (n - 2)
+    assert refs.tolist() == [1] * 4 + [0] * (pages - 4)
+    assert table[0, :3].tolist() == [0, 1, 2] and table[1, 0].item() == 3
