@@ -11,6 +11,7 @@
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
+#include <c10/hip/HIPFunctions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/torch.h>
 
@@ -97,7 +98,7 @@ struct CallStream {
     void* raw;
     explicit CallStream(Args& a) {
         PyObject* o = a.next();
-        device.reset_device(*a.device);
+        if (c10::hip::current_device() != a.device->index()) device.reset_device(*a.device);
         const auto now = at::hip::getCurrentHIPStreamMasqueradingAsCUDA(a.device->index());
         raw = now.stream();
         if (o == Py_None) return;
