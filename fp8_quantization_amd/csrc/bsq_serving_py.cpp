@@ -12,6 +12,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPFunctions.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/torch.h>
 
@@ -271,8 +272,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
             PyErr_SetObject(g_bsq_error, e);
             Py_DECREF(e);
         }
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {                  // torch's own: its Python class (OutOfMemoryError)
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }
