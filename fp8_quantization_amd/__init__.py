@@ -5,6 +5,8 @@ Argument marshalling only.  Every step of the computation runs in the HIP
 kernels of ``libbsq.so``; torch provides device memory (``torch.empty``),
 pointers (``data_ptr``) and the current stream.  There is no CPU fallback:
 if the library is not built, importing this package raises ``ImportError``.
+The operators of a decode step (``serving.py``) are names of this package too;
+their libraries are loaded, and missed, when one of them is first used.
 
 The functions carry the names of the C ABI's entry points (``include/bsq.h``);
 the quantizers are the MI355X counterparts of the launchers on the Modular
@@ -469,7 +471,22 @@ def _ceiling():
     return _ceiling_lib
 
 
-# the serving operators: 8-bit KV cache, its pages, mixture of experts for a few tokens
-from .serving import (KV_PAGE, KvCache, kv_cache, kv_cache_append, kv_cache_attention,  # noqa: E402
-                      kv_pages_compact, kv_pages_copy, kv_pages_fork, kv_pages_free,
-                      kv_pages_reserve, moe_few_tokens, serving_lib)
+# The serving operators (8-bit KV cache, its pages, mixture of experts for a few tokens) have
+# libraries of their own, loaded when one of these names is first used.
+_SERVING = ("KV_PAGE", "KvCache", "kv_cache", "kv_cache_append", "kv_cache_attention",
+            "kv_pages_compact", "kv_pages_copy", "kv_pages_fork", "kv_pages_free",
+            "kv_pages_reserve", "moe_few_tokens", "serving_lib")
+
+
+def __getattr__(name):
+    if name != "serving" and name not in _SERVING:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+
+    serving = importlib.import_module(".serving", __name__)
+    globals().update({n: getattr(serving, n) for n in _SERVING})
+    return serving if name == "serving" else getattr(serving, name)
+
+
+def __dir__():
+    return sorted({*globals(), *_SERVING, "serving"})

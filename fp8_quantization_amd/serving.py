@@ -22,11 +22,13 @@ from . import BsqError, _fmt
 
 KV_PAGE = 64
 
-LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbsq_serving.so")
+_HERE = os.path.dirname(os.path.abspath(__file__))
+LIB_PATH = os.path.join(_HERE, "libbsq_serving.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is not built; run fp8_quantization_amd/build.py "
-                      "(or __graft_entry__.build()) first")
+for _path in (LIB_PATH, os.path.join(_HERE, "_serving.so")):
+    if not os.path.exists(_path):
+        raise ImportError(f"{_path} is not built; run fp8_quantization_amd/build.py "
+                          "(or __graft_entry__.build()) first")
 
 _lib = ctypes.CDLL(LIB_PATH)
 _lib.bsq_serving_last_error.restype = ctypes.c_char_p
