@@ -40,12 +40,12 @@ FLAGS = [
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    """Build libbsq.so, libbsq_serving.so and libbsq_ceiling.so; returns the path of the
-    first."""
+    """Build libbsq.so, libbsq_serving.so, libbsq_ceiling.so and, where torch is, the extension
+    over the second; returns the path of the first."""
     _build_one(LIB, SOURCES, verbose, extra)
     _build_one(SERVING_LIB, SERVING_SOURCES, verbose, extra)
-    _build_ext(verbose)
     _build_one(CEILING_LIB, CEILING_SOURCES, verbose, extra)
+    _build_ext(verbose)
     return LIB
 
 
@@ -55,25 +55,41 @@ def _build_one(lib, sources, verbose, extra):
 
 
 def _build_ext(verbose):
-    """_serving.so: host C++ only, beside the library it links."""
+    """_serving.so: host C++ only, beside the library it links.  It needs torch and the headers of
+    torch and Python; users of the C ABI do not, so without them it is left out."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
 
-    base = os.path.dirname(os.path.abspath(torch.__file__))
-    include = os.path.join(base, "include")
+        base = os.path.dirname(os.path.abspath(torch.__file__))
+    except ImportError:
+        return _no_ext("torch")
+    include, python = os.path.join(base, "include"), sysconfig.get_paths()["include"]
+    for header in (os.path.join(include, "torch", "csrc", "Exceptions.h"),
+                   os.path.join(python, "Python.h")):
+        if not os.path.exists(header):
+            return _no_ext(header)
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     tmp = SERVING_EXT + ".tmp"
     _compile(SERVING_EXT, [
-        "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
+        HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+        "-Wno-unknown-pragmas", "-Wno-unused-command-line-argument",
         "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
         "-I" + os.path.join(ROOT, "include"), "-I" + include,
         "-I" + os.path.join(include, "torch", "csrc", "api", "include"),
-        "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(rocm, "include"),
+        "-I" + python, "-I" + os.path.join(rocm, "include"),
         os.path.join(CSRC, "bsq_serving_py.cpp"), "-o", tmp, "-L" + HERE, "-l:libbsq_serving.so",
         "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10",
         "-lc10_hip", "-Wl,-rpath,$ORIGIN"], tmp, verbose)
+
+
+def _no_ext(missing):
+    """No extension rather than one of another build."""
+    sys.stderr.write(f"_serving.so (Python binding of libbsq_serving.so) not built: no {missing}\n")
+    if os.path.exists(SERVING_EXT):
+        os.remove(SERVING_EXT)
 
 
 def _compile(lib, cmd, tmp, verbose):

@@ -84,3 +84,48 @@ else:
     raise SystemExit("not refused")
 """)
     assert res.returncode == 0, res.stdout + res.stderr
+
+
+# ------------------------------------------------------------------ building
+
+
+@pytest.fixture()
+def build(monkeypatch):
+    """The build script, its compiler calls recorded instead of run: (module, library names)."""
+    import importlib.util
+
+    spec = importlib.util.spec_from_file_location("bsq_build_of_a_test", os.path.join(PACKAGE, "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    calls = []
+    monkeypatch.setattr(mod, "_compile", lambda lib, cmd, tmp, verbose: calls.append((os.path.basename(lib), cmd)))
+    return mod, calls
+
+
+C_LIBS = ["libbsq.so", "libbsq_serving.so", "libbsq_ceiling.so"]
+
+
+def test_extension_is_built_last_and_with_hipccs_compiler(build):
+    mod, calls = build
+    assert os.path.basename(mod.build()) == "libbsq.so"
+    assert [n for n, _ in calls] == C_LIBS + ["_serving.so"]
+    assert all(cmd[0] == mod.HIPCC for _, cmd in calls)
+
+
+@pytest.mark.parametrize("what", ["torch", "headers"])
+def test_c_libraries_are_built_without_torch(build, what, monkeypatch, tmp_path, capsys):
+    """No torch, or one without headers: the C libraries, a note, and no extension left over from
+    another build."""
+    mod, calls = build
+    if what == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    else:
+        import torch
+
+        monkeypatch.setattr(torch, "__file__", str(tmp_path / "torch" / "__init__.py"))
+    monkeypatch.setattr(mod, "SERVING_EXT", str(tmp_path / "_serving.so"))
+    (tmp_path / "_serving.so").write_bytes(b"of another build")
+    mod.build()
+    assert [n for n, _ in calls] == C_LIBS
+    assert not (tmp_path / "_serving.so").exists()
+    assert "_serving.so" in capsys.readouterr().err
