@@ -16,11 +16,17 @@ def test_out_of_memory_is_torchs_error(bsq):  # noqa: F811
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     total = torch.cuda.get_device_properties(0).total_memory
+    held = []
     try:
         torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (32 << 20)) / total)
+        # what earlier tests left in the allocator may be free for `out`: taken until nothing is
+        with pytest.raises(torch.OutOfMemoryError):
+            for _ in range(10000):
+                held.append(torch.empty_like(q))
         with pytest.raises(torch.OutOfMemoryError):
             bsq.kv_cache_attention(*args)
     finally:
+        del held
         torch.cuda.set_per_process_memory_fraction(1.0)
     out = bsq.kv_cache_attention(*args)
     torch.cuda.synchronize()
