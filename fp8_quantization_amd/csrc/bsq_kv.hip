@@ -940,9 +940,7 @@ template <int D>
 void append(const AppendArgs& a, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.seqs.num_seqs * a.pages_per_seq),
                     (uint32_t)a.cache.num_heads, 2);
-    // up to 5 tokens lie in two groups of 4: one wave's work (64 sequences of 5 tokens, 8 heads
-    // of 128: 6.2 us a call, with 256 threads 8.1)
-    if (a.max_new <= 5)
+    if (append_threads(a.max_new) == 64)
         hipLaunchKernelGGL((kv_append_kernel<D, 64, 2>), grid, dim3(64), 0, stream, a);
     else
         hipLaunchKernelGGL((kv_append_kernel<D, kThreads, 16>), grid, dim3(kThreads), 0, stream, a);
@@ -1004,6 +1002,7 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     // little work: eight waves share a run, so each walks half as many pages (8 sequences of 777
     // tokens 8.8 us, with four 10.8; 64 of 8192 145 and 115)
     if (!p.rows_form) p.wide = blocks * p.splits <= 512;
+    p.threads = p.wide || (p.rows_form && head_dim == 256) ? 512 : 256;
     p.split_pages = (int32_t)run;
     return p;
 }

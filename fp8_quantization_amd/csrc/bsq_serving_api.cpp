@@ -37,6 +37,10 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
 
+// Whether a launch may have that many workgroups: its threads are counted in 32 bits.
+bool fits(double workgroups, int threads) { return workgroups <= (double)(0xFFFFFFFFu / threads); }
+constexpr int kPageThreads = 256;    // of every kernel with a workgroup per request
+
 // Head count, head width and page count of a cache; with data, its buffers too.
 int check_cache(const bsq_kv_cache* c, bsq::KvCache* out) {
     if (!c) return fail(BSQ_ERR_INVALID_ARG, "null pointer (cache)");
@@ -141,7 +145,8 @@ int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_s
     *p = bsq::plan_attend(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window);
     const double blocks = (double)num_seqs * (double)num_heads * (double)p->col_blocks * p->splits;
     const double pairs = (double)num_seqs * (double)max_q * (double)num_q_heads;
-    if (blocks > (double)kMaxInt || (p->splits > 1 && pairs > (double)kMaxInt))
+    // the join has at least a wave for each pair
+    if (!fits(blocks, p->threads) || (p->splits > 1 && !fits(pairs, 64)))
         return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
     return BSQ_OK;
 }
@@ -163,7 +168,8 @@ int check_pages(const bsq_kv_cache* cache, const void* a, const void* b, int64_t
     p->n = (int32_t)n;
     // one workgroup for each 16 KiB of a page and request
     const int64_t parts = 2 * (int64_t)p->cache.num_heads * p->cache.head_dim * bsq::kKvPage / 16384 + 2;
-    if (n * parts > kMaxInt) return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
+    if (!fits((double)(n * parts), kPageThreads))
+        return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
     return BSQ_OK;
 }
 
@@ -202,7 +208,7 @@ int kv_cache_append(const bsq_kv_cache* cache, const void* k, int64_t ldk, const
     // max_new tokens touch one page more than they fill when they start inside one
     int64_t pages = (max_new + bsq::kKvPage - 2) / bsq::kKvPage + 1;
     if (pages > max_pages) pages = max_pages;
-    if (num_seqs * pages > kMaxInt)
+    if (!fits((double)(num_seqs * pages), bsq::append_threads(max_new)))
         return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
     a.pages_per_seq = (int32_t)pages;
     a.max_new = (int32_t)max_new;
@@ -331,6 +337,8 @@ int kv_pages_free(const int32_t* block_table, int64_t table_stride, int64_t max_
     if (st == BSQ_OK) st = check_slots(num_pages, refcounts, slots, n);
     if (st != BSQ_OK) return st;
     if (n == 0) return ok();
+    if (!fits((double)n, kPageThreads))
+        return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
     p.cache.num_pages = (int32_t)num_pages;
     p.table = const_cast<int32_t*>(block_table);   // read only
     p.table_stride = table_stride;
