@@ -31,7 +31,24 @@ for _path in (LIB_PATH, os.path.join(_HERE, "_serving.so")):
                           "(or __graft_entry__.build()) first")
 
 _lib = ctypes.CDLL(LIB_PATH)
-_lib.bsq_serving_last_error.restype = ctypes.c_char_p
+_i64, _i32, _p, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
+for _name, _res, *_args in (
+        ("kv_cache_append", _i32, _p, _p, _i64, _p, _i64, _p, _p, _p, *[_i64] * 5, _p),
+        ("kv_cache_attention", _i32, _p, _p, _i64, _i64, _p, _p, _p, *[_i64] * 6, _f32, _i64, _p,
+         _i64, _p, _p, _i64, _p),
+        ("kv_cache_attention_workspace", _i64, *[_i64] * 8),
+        ("kv_pages_copy", _i32, _p, _p, _p, _i64, _p),
+        ("kv_pages_reserve", _i32, _p, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _p, _p),
+        ("kv_pages_fork", _i32, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _p, _p),
+        ("kv_pages_free", _i32, _p, _i64, _i64, _i64, _p, _p, _i64, _p, _i64, _p),
+        ("kv_pages_compact", _i32, _p, _p, _i64, _i64, _i64, _p, _p, _p, _i64, _p, _p, _p, _i64,
+         _p),
+        ("kv_pages_compact_workspace", _i64, _i64),
+        ("moe_few_tokens", _i32, _i32, _p, *[_i64] * 6, _p, _p, _p, _p, _p, _i32, _p, _p, _p, _i64,
+         _p, _i64, _p),
+        ("moe_few_tokens_workspace", _i64, *[_i64] * 4),
+        ("bsq_serving_last_error", ctypes.c_char_p)):
+    getattr(_lib, _name).restype, getattr(_lib, _name).argtypes = _res, _args
 
 from . import _serving  # noqa: E402  (built beside LIB_PATH, which it links)
 
