@@ -498,11 +498,12 @@ constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
 template <int FMT>
 __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArgs a) {
     constexpr int CH = kShort<FMT>, S = 128 * CH;
-    __shared__ float sums[kDownWaves][16 * 16];    // [token][column]
+    // [token][4 columns]: as vectors, so that their 16-byte accesses are aligned
+    __shared__ f32x4 sums[kDownWaves][16 * 4];
     const int tid = (int)threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int entries = a.tokens * a.topk;
-    for (int k = lane; k < 16 * 16; k += 64) sums[wave][k] = 0.0f;
+    sums[wave][lane] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     const FewEntries few =
         few_entries(a, lane < entries ? a.ids[lane] : -1, lane < entries ? a.weights[lane] : 0.0f,
                     a.logits != nullptr);
@@ -568,8 +569,8 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
         if (it + 1 < it_to && it + 1 < (ai + 1) * steps) return;
         const float f = __shfl(few.w, item.row);
         if (r16 < item.n) {
-            f32x4* s = reinterpret_cast<f32x4*>(&sums[wave][item.row / a.topk * 16 + 4 * g]);
-            *s = *s + acc * f;
+            f32x4& s = sums[wave][item.row / a.topk * 4 + g];
+            s = s + acc * f;
         }
         acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     };
@@ -589,9 +590,9 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_few_kernel(const MoeArg
     }
     __syncthreads();
     for (int k = tid; k < a.tokens * 16; k += kDownThreads) {
-        float y = sums[0][k];
+        float y = reinterpret_cast<const float*>(sums[0])[k];
 #pragma unroll
-        for (int w = 1; w < kDownWaves; ++w) y += sums[w][k];
+        for (int w = 1; w < kDownWaves; ++w) y += reinterpret_cast<const float*>(sums[w])[k];
         reinterpret_cast<__bf16*>(a.y)[k / 16 * a.ldy + col0 + k % 16] = (__bf16)y;
     }
 }
