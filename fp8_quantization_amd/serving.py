@@ -121,7 +121,9 @@ def kv_pages_reserve(block_table: torch.Tensor, kv_lens: torch.Tensor, refcounts
                      slots: torch.Tensor, add_tokens: torch.Tensor, status=None, stream=None):
     """Lengthen sequences slots[i] by add_tokens[i] tokens, with pages of
     refcount 0, lowest number first, requests in order.  Returns status
-    (int32: 0 done, 1 no pages or table entries left, 2 no such slot)."""
+    (int32: 0 done, 1 no pages or table entries left, 2 no such slot).  To take
+    tokens back, lower ``kv_lens``, after taking 1 off the ``refcounts`` of the
+    pages at the row's end that this gives up."""
     return _serving.pages_reserve(block_table, kv_lens, refcounts, slots, add_tokens, status,
                                   stream)
 

@@ -163,6 +163,15 @@ int64_t kv_cache_attention_workspace(int64_t num_heads, int64_t head_dim, int64_
  * slot once (children of a fork: distinct slots that no request names as a
  * parent).
  *
+ * No call shortens a sequence.  A caller that takes back its last tokens (a
+ * proposal that was not accepted) writes the smaller number to kv_lens itself.
+ * Where fewer pages hold it then, ceil(kv_lens / 64), it first takes 1 off the
+ * counts of the pages that are given up: the last entries of the sequence's
+ * table row.  Left counted they are free for no one, and the next reserve
+ * writes over the entries that name them.  The next append then writes over
+ * the tokens taken back; in a page that it shares with tokens that stay, the
+ * scale is at least what they had made it.
+ *
  * kv_pages_copy     page dst[i] becomes a copy of page src[i] (codes and
  *     scales of every head).  Distinct destinations, none of them a source
  *     of another pair.  Pairs outside the cache are skipped.

@@ -136,3 +136,40 @@ def test_needs_past_32_bits(bsq, n, width):  # noqa: F811
     assert lens.tolist() == [130, 1] + [0] * (n - 2)
     assert refs.tolist() == [1] * 4 + [0] * (pages - 4)
     assert table[0, :3].tolist() == [0, 1, 2] and table[1, 0].item() == 3
+
+
+@pytest.mark.parametrize("kept", [64, 70, 128, 129, 150])
+def test_tokens_taken_back(bsq, kept):  # noqa: F811
+    """A sequence is shortened as the header says: the pages given up are given out again, and
+    what is appended then is what a sequence holds that never had the other tokens."""
+    rng = np.random.default_rng(kept)
+    L, D, more = 150, 64, 90
+    x = R.bf16(rng.standard_normal((L, 1, D)))
+    y = R.bf16(rng.standard_normal((more, 1, D)))
+    y[0] = 7.9                                               # no smaller scale than x's
+    d, c = bsq.kv_cache(6, 1, D), R.Cache(6, 1, D)
+    table, lens = torch.full((2, 6), -1, dtype=torch.int32, device="cuda"), i32([0, 0])
+    refs = i32([0] * 6)
+
+    def reserve(slot, n):
+        assert bsq.kv_pages_reserve(table, lens, refs, i32([slot]), i32([n])).tolist() == [0]
+    reserve(0, L)
+    bsq.kv_cache_append(d, dev_rows(x), dev_rows(x), i32([0, L, L]), lens, table, L)
+    up = table[0, -(-kept // 64):-(-L // 64)].long()
+    refs[up] -= 1
+    lens[0] = kept
+    reserve(1, 64)                                           # a page given up, where there is one
+    reserve(0, more)
+    bsq.kv_cache_append(d, dev_rows(y), dev_rows(y), i32([0, more, more]), lens, table, more)
+    torch.cuda.synchronize()
+    rows = [table[0].tolist()]
+    R.append(c, x[:kept], x[:kept], [0, kept], [kept], rows)
+    R.append(c, y, y, [0, more], [kept + more], rows)
+    assert lens.tolist() == [kept + more, 64]
+    assert refs.tolist() == [1] * (-(-(kept + more) // 64) + 1) + [0] * (5 - -(-(kept + more) // 64))
+    got = [t.cpu().numpy() for t in d]
+    for p in range(-(-(kept + more) // 64)):
+        page, n = rows[0][p], min(64, kept + more - 64 * p)
+        assert np.array_equal(got[0][page, 0, :, :n], c.k[page, 0, :, :n])
+        assert np.array_equal(got[1][page, 0][:, R.v_place(np.arange(n))], c.v[page, 0][:, R.v_place(np.arange(n))])
+        assert got[2][page, 0] == c.ks[page, 0] and got[3][page, 0] == c.vs[page, 0]
