@@ -554,10 +554,12 @@ __device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq,
 
 // Few columns (decode): a workgroup takes 16 columns of one (sequence, head)
 // and a run of their pages, its W waves every W-th page; their states meet
-// in LDS at the end.  ONCE: no other workgroup reads these pages (one block of
-// columns), so they are loaded past the caches' retention.  Bound by the pages'
-// bytes: 64 sequences of 8192 tokens, 32 heads on 8 of 128, take 111 us (6.1
-// TB/s; 132 without ONCE).
+// in LDS at the end.  ONCE: no other workgroup of the sequence reads these pages
+// (one block of columns), so they are loaded past the caches' retention.  Bound by
+// the pages' bytes: 64 sequences of 8192 tokens, 32 heads on 8 of 128, take 112 us
+// (6.0 TB/s; a call 115, without ONCE 131).  Sequences that share their pages pay
+// for it, as the host does not know of them: 64 forks of one such prompt take 78 us
+// a call and would take 61, 8 of 100000 tokens 246 and 222 (apart 183 and 205).
 template <int D, int W, bool ONCE>
 __global__ void __launch_bounds__(64 * W, D == 256 ? 1 : W == 4 ? 3 : 2)
 attend_split_kernel(const AttendArgs a) {
@@ -892,8 +894,10 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
 // that two do at 128), and columns of its workgroup, narrow and wide.  A wide one's eight
 // waves share the conversion of a page, half the work of two narrow ones, but end together:
 // with 32 heads of 128, 2 sequences of 2048 rows in 8192 tokens (512 wide workgroups) take
-// 368 us wide and 398 narrow, 2 of 1024 in 4000 (256) 123 and 112.  head_dim 64 is narrow (its
-// page is too small for 512 threads), 256 has eight waves at 128 columns.
+// 339 us wide and 361 narrow, 2 of 1024 in 4000 (256) 157 and 112.  Between them wide is the
+// faster already: 1792 rows (448) 333 and 348, 1500 (384) 327 and 338, 1280 (320) 289 and 320.
+// head_dim 64 is narrow (its page is too small for 512 threads), 256 has eight waves at 128
+// columns.
 template <int D>
 constexpr int kRowBlocks = D == 256 ? 1 : 2;
 constexpr int kRowColumns = 128, kWideColumns = 256;

@@ -327,10 +327,13 @@ __device__ __forceinline__ int many_entries(const MoeArgs& a, ManyEntries& m, in
 // the rows of W1 and those of W3 that belong to them, over all of `hidden`, its
 // waves taking contiguous runs of the steps.  16 NB entries at a time are the
 // matrix columns; columns past the last repeat it, and no result of theirs is
-// stored.  Bound by the weights' bytes, at what loads three or four waves of a
-// SIMD keep on their way: 394 MB in 86 us in FP4 (4.6 TB/s), 553 MB in 102 us
-// in E4M3 (5.4 TB/s).  More waves with fewer registers, steps loaded ahead in
-// each wave, or two or eight waves a workgroup were no faster.
+// stored.  Bound by the weights' bytes and by its workgroups' rounds: 394 MB in
+// 86 us in FP4 (4.6 TB/s) and 553 MB in 100 us in E4M3 (5.5 TB/s) are some 1630
+// and 2048 workgroups with work, 2.1 and 2.7 times the 768 that fit (three waves a
+// SIMD), and the CUs hold work in 79% and 88% of that time (SQ_BUSY_CU_CYCLES over
+// GRBM_GUI_ACTIVE): while they do, the weights come at 5.8 and 6.3 TB/s.  More waves
+// with fewer registers, steps loaded ahead in each wave, or two or eight waves a
+// workgroup were no faster.
 
 constexpr int kUpWaves = 4, kUpThreads = 64 * kUpWaves;
 constexpr float kBf16Max = 0x1.FEp127f;
@@ -863,9 +866,10 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
     // they would read their weights again.  64 tokens, 4096 x 1024 in E4M3: 4 of 64 experts (4 an
     // expert) 158 us and 167 with two, 2 of 8 (16 an expert) 60 and 56.
     const bool narrow = a.tokens <= 16 || entries <= 10 * a.experts;
-    // Wide tiles (x read once for twice the weights) where they give workgroups enough: 16 tokens
-    // (1536 wide tiles, 2048 x 768) 68.5 us and 75.8 narrow, 4 (768) 33.5 and 35.3; but 1 token
-    // (128, 7168 x 512) 29.5 and 24.9.
+    // Wide tiles (x read once for twice the weights) where they give workgroups enough, 8 experts a
+    // token: of 128 (2048 x 768) 16 tokens (3072 wide tiles) take 68.7 us and 76.1 narrow, 8 (1536)
+    // 48.2 and 51.9, 4 (768) 33.6 and 35.0, 2 (384) 24.8 and 23.6; of 256 (7168 x 512) 16 tokens
+    // (2048) 149 and 152, 8 (1024) 95.2 and 92.5, 4 (512) 59.1 and 60.4, 1 (128) 29.7 and 24.9.
     if (units * (a.inter / 32) >= 768) {
         if (narrow) launch_up<FMT, 1, 2>(a, few, routed, stream);
         else launch_up<FMT, 2, 2>(a, few, routed, stream);
