@@ -262,7 +262,7 @@ int kv_cache_attention(const bsq_kv_cache* cache, const void* q, int64_t ldq, in
     a.part_o = static_cast<float*>(workspace);
     if (need > 0)
         a.part_ml = a.part_o + (int64_t)p.splits * num_rows * num_q_heads * cache->head_dim;
-    a.window = window;
+    a.window = window > kMaxInt ? 0 : window;      // longer than any sequence; its places stay in 64 bits
     a.scale = scale;
     a.num_q_heads = (int32_t)num_q_heads;
     a.group = (int32_t)(num_q_heads / cache->num_heads);

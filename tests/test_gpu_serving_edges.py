@@ -29,6 +29,19 @@ def test_nan_page_that_a_row_does_not_see(bsq, D, heads, vs, rows, L, window):  
     assert np.isnan(out).any() and np.isfinite(out).any()
 
 
+@pytest.mark.parametrize("rows", [10, 80])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1])
+def test_windows_longer_than_any_sequence(bsq, rows, window):  # noqa: F811
+    """As no window, also where a sequence has rows before its first token."""
+    lens = [rows - 7, 300, 3]
+    c, q, off, table = make(rows, [rows, 300, rows], [rows] * 3, 2, 4, 64)
+    got = attend(bsq, c, q, off, lens, table, 0.1, window)
+    want = attend(bsq, c, q, off, lens, table, 0.1)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.isfinite(want[1][7:rows]).all()
+
+
 # ------------------------------------------------------------------ experts
 
 
