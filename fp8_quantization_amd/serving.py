@@ -123,7 +123,8 @@ def kv_pages_reserve(block_table: torch.Tensor, kv_lens: torch.Tensor, refcounts
     refcount 0, lowest number first, requests in order.  Returns status
     (int32: 0 done, 1 no pages or table entries left, 2 no such slot).  To take
     tokens back, lower ``kv_lens``, after taking 1 off the ``refcounts`` of the
-    pages at the row's end that this gives up."""
+    pages at the row's end that this gives up; the page that it ends in must be
+    the sequence's own (``include/bsq_serving.h``)."""
     return _serving.pages_reserve(block_table, kv_lens, refcounts, slots, add_tokens, status,
                                   stream)
 

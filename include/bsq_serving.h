@@ -169,8 +169,11 @@ int64_t kv_cache_attention_workspace(int64_t num_heads, int64_t head_dim, int64_
  * counts of the pages that are given up: the last entries of the sequence's
  * table row.  Left counted they are free for no one, and the next reserve
  * writes over the entries that name them.  The next append then writes over
- * the tokens taken back; in a page that it shares with tokens that stay, the
- * scale is at least what they had made it.
+ * the tokens taken back; in a page where others stay, the scale is at least
+ * what they had made it.  A page that is partly filled afterwards must be the
+ * sequence's own, as for any append: one that a fork shares (a count above 1)
+ * is first exchanged for a copy, a free page with count 1 (kv_pages_copy, its
+ * number in the table, and 1 off the shared page's count).
  *
  * kv_pages_copy     page dst[i] becomes a copy of page src[i] (codes and
  *     scales of every head).  Distinct destinations, none of them a source
