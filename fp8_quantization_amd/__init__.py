@@ -475,7 +475,7 @@ def _ceiling():
 # libraries of their own, loaded when one of these names is first used.
 _SERVING = ("KV_PAGE", "KvCache", "kv_cache", "kv_cache_append", "kv_cache_attention",
             "kv_pages_compact", "kv_pages_copy", "kv_pages_fork", "kv_pages_free",
-            "kv_pages_reserve", "moe_few_tokens", "serving_lib")
+            "kv_pages_reserve", "moe_few_tokens", "qk_norm_rope", "serving_lib")
 
 
 def __getattr__(name):

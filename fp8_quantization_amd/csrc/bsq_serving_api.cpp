@@ -1,5 +1,5 @@
 // bsq_serving_api.cpp -- the C ABI of libbsq_serving (declared in
-// include/bsq_serving.h): argument validation, launch geometry and error
+// include/bsq_serving.h and include/bsq_decoder.h): argument validation, launch geometry and error
 // reporting.  Every check runs on the host before any HIP call.
 #include <hip/hip_runtime.h>
 
@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <string>
 
+#include "bsq_decoder.h"
 #include "bsq_serving.h"
 #include "bsq_serving_internal.h"
 
@@ -97,6 +98,12 @@ int check_rows(const char* what, const void* p, int64_t ld, int64_t width) {
     if (ld < width || ld % 8 != 0)
         return fail(BSQ_ERR_INVALID_ARG, "the row stride %lld of %s must be >= %lld and a multiple of 8",
                     (long long)ld, what, (long long)width);
+    return BSQ_OK;
+}
+
+int check_dtype(int dtype) {
+    if (dtype != BSQ_BF16 && dtype != BSQ_FP32)
+        return fail(BSQ_ERR_UNSUPPORTED, "dtype %d is not provided (BF16 or FP32)", dtype);
     return BSQ_OK;
 }
 
@@ -467,6 +474,76 @@ int moe_few_tokens(int format, const void* x, int64_t ldx, int64_t num_tokens, i
     a.topk = (int32_t)topk;
     a.renormalize = renormalize;
     return launched(bsq::launch_moe(format, a, static_cast<hipStream_t>(stream)));
+}
+
+int qk_norm_rope(int dtype, const void* q, int64_t ldq, int64_t num_q_heads, const void* k,
+                 int64_t ldk, int64_t num_heads, const void* v, int64_t ldv, int64_t head_dim,
+                 int64_t num_rows, const float* q_weight, const float* k_weight, float eps,
+                 const int32_t* positions, const double* inv_freq, int64_t rotary_dim,
+                 int interleaved, void* q_out, int64_t ldqo, void* k_out, int64_t ldko, void* v_out,
+                 int64_t ldvo, void* stream) {
+    int st = check_dtype(dtype);
+    if (st != BSQ_OK) return st;
+    if (head_dim < 8 || head_dim > 256 || head_dim % 8 != 0)
+        return fail(BSQ_ERR_UNSUPPORTED, "head_dim=%lld is not provided (multiples of 8, 8 .. 256)",
+                    (long long)head_dim);
+    if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16 != 0)
+        return fail(BSQ_ERR_UNSUPPORTED,
+                    "rotary_dim=%lld is not provided (multiples of 16, 0 .. head_dim=%lld)",
+                    (long long)rotary_dim, (long long)head_dim);
+    if (num_q_heads < 1 || num_q_heads > 65535 || num_heads < 1 || num_heads > 65535)
+        return fail(BSQ_ERR_INVALID_ARG, "num_q_heads=%lld and num_heads=%lld must be in 1 .. 65535",
+                    (long long)num_q_heads, (long long)num_heads);
+    if (num_rows < 0 || num_rows > kMaxInt)
+        return fail(BSQ_ERR_INVALID_ARG, "num_rows=%lld must be in 0 .. 2^31 - 1",
+                    (long long)num_rows);
+    if (!std::isfinite(eps) || eps < 0.0f)
+        return fail(BSQ_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (!v != !v_out) return fail(BSQ_ERR_INVALID_ARG, "v and v_out: both or neither");
+    if (num_rows == 0) return ok();
+    const int64_t qw = num_q_heads * head_dim, kw = num_heads * head_dim;
+    if ((st = check_rows("q", q, ldq, qw)) != BSQ_OK) return st;
+    if ((st = check_rows("k", k, ldk, kw)) != BSQ_OK) return st;
+    if ((st = check_rows("q_out", q_out, ldqo, qw)) != BSQ_OK) return st;
+    if ((st = check_rows("k_out", k_out, ldko, kw)) != BSQ_OK) return st;
+    if (v) {
+        if ((st = check_rows("v", v, ldv, kw)) != BSQ_OK) return st;
+        if ((st = check_rows("v_out", v_out, ldvo, kw)) != BSQ_OK) return st;
+    }
+    if (!positions || !inv_freq) {
+        if (rotary_dim > 0)
+            return fail(BSQ_ERR_INVALID_ARG, "null pointer (positions=%p inv_freq=%p)", positions,
+                        inv_freq);
+    }
+    if (!aligned(positions, 4) || !aligned(inv_freq, 8) || !aligned(q_weight, 4) ||
+        !aligned(k_weight, 4))
+        return fail(BSQ_ERR_INVALID_ARG, "positions, inv_freq and weights must be aligned to their size");
+    bsq::RopeArgs a{};
+    const void* x[3] = {q, k, v};
+    void* out[3] = {q_out, k_out, v_out};
+    const int64_t ldx[3] = {ldq, ldk, ldv}, ldo[3] = {ldqo, ldko, ldvo};
+    const int64_t heads[3] = {num_q_heads, num_heads, v ? num_heads : 0};
+    for (int i = 0; i < 3; ++i) {
+        a.x[i] = x[i];
+        a.out[i] = static_cast<uint16_t*>(out[i]);
+        a.ldx[i] = ldx[i];
+        a.ldo[i] = ldo[i];
+        a.heads[i] = (int32_t)heads[i];
+    }
+    a.weight[0] = q_weight;
+    a.weight[1] = k_weight;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.num_rows = num_rows;
+    a.eps = eps;
+    a.inv_dim = 1.0f / (float)head_dim;
+    a.head_dim = (int32_t)head_dim;
+    a.rotary_dim = (int32_t)rotary_dim;
+    bsq::plan_rope(a);
+    if (!fits((double)num_rows * a.parts, 64) || num_rows * a.parts > kMaxInt - 4)
+        return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
+    return launched(bsq::launch_rope(a, dtype == BSQ_FP32, interleaved != 0,
+                                     static_cast<hipStream_t>(stream)));
 }
 
 const char* bsq_serving_last_error(void) { return g_last_error; }

@@ -1,6 +1,6 @@
 // bsq_serving_internal.h -- launch interface between the host layer of
 // libbsq_serving (bsq_serving_api.cpp) and its gfx950 kernels (bsq_kv.hip,
-// bsq_moe.hip).  Not installed.
+// bsq_pages.hip, bsq_moe.hip, bsq_rope.hip).  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -141,5 +141,22 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTopk = 16;
 constexpr int kFewEntries = 16;
 inline bool moe_is_few(int64_t tokens, int64_t topk) { return tokens * topk <= kFewEntries; }
 hipError_t launch_moe(int fmt, const MoeArgs& a, hipStream_t stream);
+
+struct RopeArgs {
+    const void* x[3];                // q, k, v
+    uint16_t* out[3];
+    int64_t ldx[3], ldo[3];          // elements
+    int32_t heads[3];                // v: 0 where there is none
+    const float* weight[2];          // nullable
+    const int32_t* positions;
+    const double* inv_freq;
+    int64_t num_rows;
+    float eps, inv_dim;
+    int32_t head_dim, rotary_dim;
+    int32_t seg_steps[3], all_steps; // steps (of as many heads as a wave takes at once) of a row
+    int32_t steps, parts;            // of a wave; waves of a row
+};
+void plan_rope(RopeArgs& a);         // seg_steps and what follows, from the sizes
+hipError_t launch_rope(const RopeArgs& a, bool f32, bool pairs, hipStream_t stream);
 
 }  // namespace bsq

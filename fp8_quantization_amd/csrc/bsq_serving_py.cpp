@@ -20,6 +20,7 @@
 #include <cstdio>
 #include <string>
 
+#include "bsq_decoder.h"
 #include "bsq_serving.h"
 
 namespace {
@@ -172,6 +173,13 @@ void* matrix(const at::Tensor* t, const char* name, at::ScalarType dtype, int64_
         refuse(BSQ_ERR_INVALID_ARG, "%s is [%lld, %lld]; it must be [%lld, %lld]", name,
                (long long)t->size(0), (long long)t->size(1), (long long)rows, (long long)cols);
     return t->data_ptr();
+}
+
+// BSQ_BF16 or BSQ_FP32.
+int dtype_of(const at::Tensor& t, const char* name) {
+    if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
+        refuse(0, "%s must be a bfloat16 or float32 GPU tensor", name);
+    return t.scalar_type() == at::kFloat ? BSQ_FP32 : BSQ_BF16;
 }
 
 // Rows of BF16, dense within a row.
@@ -543,6 +551,65 @@ PyObject* moe(Args& a) {
     return r;
 }
 
+// q, k, v, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out, v_out, stream
+// -> (q, k, v or None)
+PyObject* rope(Args& a) {
+    static const char* const names[3] = {"q", "k", "v"};
+    static const char* const outs[3] = {"q_out", "k_out", "v_out"};
+    const at::Tensor* x[3] = {a.tensor("q"), a.tensor("k"), a.tensor("v", true)};
+    const at::Tensor* positions = a.tensor("positions");
+    const at::Tensor* freq = a.tensor("inv_freq");
+    const at::Tensor* weight[2] = {a.tensor("q_weight", true), a.tensor("k_weight", true)};
+    const double eps = a.number("eps");
+    const int64_t interleaved = a.integer("interleaved");
+    const at::Tensor* out[3];
+    for (int i = 0; i < 3; ++i) out[i] = a.tensor(outs[i], true);
+    const CallStream stream(a);
+    const int dtype = dtype_of(*x[0], "q");
+    for (int i = 0; i < 3; ++i) {
+        if (!x[i]) continue;
+        if (x[i]->scalar_type() != x[0]->scalar_type() || x[i]->dim() != 3 || !dense_rows(*x[i]))
+            refuse(0, "%s must be a 3-D GPU tensor of q's dtype, contiguous within a row", names[i]);
+        if (x[i]->size(0) != x[0]->size(0) || x[i]->size(2) != x[0]->size(2) ||
+            (i == 2 && x[2]->size(1) != x[1]->size(1)))
+            refuse(BSQ_ERR_INVALID_ARG,
+                   "q, k and v must be [rows, heads, width] of the same rows and width, v of k's heads");
+    }
+    const int64_t R = x[0]->size(0), D = x[0]->size(2), rot = 2 * freq->numel();
+    vec(positions, "positions", at::kInt, R, true);
+    vec(freq, "inv_freq", at::kDouble, 0, false);
+    const float* w[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; ++i)
+        if (weight[i])
+            w[i] = vec(weight[i], i ? "k_weight" : "q_weight", at::kFloat, D, true).data_ptr<float>();
+    if (!x[2] && out[2]) refuse(BSQ_ERR_INVALID_ARG, "v_out without v");
+    at::Tensor own[3];
+    for (int i = 0; i < 3; ++i) {
+        if (!x[i]) continue;
+        if (out[i]) {
+            rows_of(out[i], outs[i], 3);
+            if (out[i]->size(0) < R || out[i]->size(1) != x[i]->size(1) || out[i]->size(2) != D)
+                refuse(BSQ_ERR_INVALID_ARG, "%s must be [%lld, %lld, %lld]", outs[i], (long long)R,
+                       (long long)x[i]->size(1), (long long)D);
+        } else {
+            own[i] = empty({R, x[i]->size(1), D}, at::kBFloat16, *a.device);
+            out[i] = &own[i];
+        }
+    }
+    auto ptr = [](const at::Tensor* t) { return t ? t->data_ptr() : nullptr; };
+    auto ld = [](const at::Tensor* t) { return t ? row_stride(*t) : 0; };
+    check(qk_norm_rope(dtype, ptr(x[0]), ld(x[0]), x[0]->size(1), ptr(x[1]), ld(x[1]), x[1]->size(1),
+                       ptr(x[2]), ld(x[2]), D, R, w[0], w[1], (float)eps,
+                       positions->data_ptr<int32_t>(), freq->data_ptr<double>(), rot,
+                       (int)interleaved, ptr(out[0]), ld(out[0]), ptr(out[1]), ld(out[1]),
+                       ptr(out[2]), ld(out[2]), stream.raw));
+    PyObject* o[3] = {stream.give(*out[0], own[0]), stream.give(*out[1], own[1]),
+                      x[2] ? stream.give(*out[2], own[2]) : none()};
+    PyObject* r = o[0] && o[1] && o[2] ? PyTuple_Pack(3, o[0], o[1], o[2]) : nullptr;
+    for (PyObject* p : o) Py_XDECREF(p);
+    return r;
+}
+
 #define ENTRY(name, fn) {name, (PyCFunction)(void (*)(void))entry<fn>, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY("init", init),
                            ENTRY("append", append),
@@ -553,6 +620,7 @@ PyMethodDef g_methods[] = {ENTRY("init", init),
                            ENTRY("pages_free", pages_free),
                            ENTRY("pages_compact", pages_compact),
                            ENTRY("moe", moe),
+                           ENTRY("rope", rope),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -1,6 +1,7 @@
 """Python binding of libbsq_serving: the paged 8-bit key/value cache with its
-attention and page management, and the mixture-of-experts layer for a few
-tokens over MX weights (``include/bsq_serving.h``).
+attention and page management, the mixture-of-experts layer for a few tokens
+over MX weights (``include/bsq_serving.h``), and the operators around them in a
+decoder's step (``include/bsq_decoder.h``).
 
 Argument marshalling only, as in the package itself.  A decode step calls
 these for a few microseconds of GPU work each, so the checks and the launch
@@ -47,6 +48,8 @@ for _name, _res, *_args in (
         ("moe_few_tokens", _i32, _i32, _p, *[_i64] * 6, _p, _p, _p, _p, _p, _i32, _p, _p, _p, _i64,
          _p, _i64, _p),
         ("moe_few_tokens_workspace", _i64, *[_i64] * 4),
+        ("qk_norm_rope", _i32, _i32, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _p, _p,
+         _f32, _p, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _i64, _p),
         ("bsq_serving_last_error", ctypes.c_char_p)):
     getattr(_lib, _name).restype, getattr(_lib, _name).argtypes = _res, _args
 
@@ -169,3 +172,18 @@ def moe_few_tokens(x: torch.Tensor, fmt, w13_codes: torch.Tensor, w13_scales: to
     topk_ids, topk_weights)."""
     return _serving.moe(x, _fmt(fmt), w13_codes, w13_scales, w2_codes, w2_scales, num_experts, topk,
                         router_logits, topk_ids, topk_weights, renormalize, out, workspace, stream)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                 v=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None, v_out=None, stream=None):
+    """Norms of queries and keys for each head and their rotation by position.
+    ``q`` and ``k`` [rows, heads, D], BF16 or both FP32 (slices of one
+    projection's output do); with ``q_weight`` / ``k_weight`` (fp32 [D])
+    x * weight / sqrt(mean x^2 + eps), then the first 2 * len(inv_freq)
+    elements of a head turned by positions (int32 [rows]) * inv_freq (float64,
+    radians a token): pairs (i, i + len), or neighbours with ``interleaved``.
+    Returns BF16 (q, k, v): v is rounded only, None where none is given.  An
+    output may be its BF16 input itself."""
+    return _serving.rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out,
+                         k_out, v_out, stream)
