@@ -307,12 +307,46 @@ __device__ __forceinline__ void init_state(AttState<D, CB>& st) {
 }
 
 // What a wave needs of its columns to mask: each lane's column sees tokens
-// [first, last].
-template <int CB>
+// [first, last].  MASKED (kv_cache_attention_masked): the tokens [0, sinks) too, and of the
+// tokens from `base` on (a tree's rows) those whose bits are set.
+template <int CB, bool MASKED>
 struct Columns {
     int first[CB], last[CB];         // per lane
     int all_from, all_to;            // tokens that every column of the wave sees
 };
+template <int CB>
+struct Columns<CB, true> {
+    int first[CB], last[CB];
+    int all_from, all_to;
+    const uint64_t* mask[CB];        // per lane; null: no tree
+    int words, base, end, sinks;     // end: the sequence's length
+
+    // The lowest k bits.
+    static __device__ __forceinline__ uint64_t low(int k) {
+        return k <= 0 ? 0 : k >= 64 ? ~0ull : (1ull << k) - 1;
+    }
+    // Which tokens of the page that starts at token t column cb sees.
+    __device__ __forceinline__ uint64_t page(int cb, int t) const {
+        const uint64_t near = ~low(first[cb] - t) | low(min(sinks, end) - t);
+        if (!mask[cb]) return near & low(last[cb] + 1 - t);
+        uint64_t seen = near & low(base - t);
+        if (t + kKvPage > base) {
+            const int x = t - base, i = x >> 6, s = x & 63;   // x < 0: i is -1
+            uint64_t bits = 0;
+            if (i >= 0 && i < words) bits = mask[cb][i] >> s;
+            if (s && i + 1 < words) bits |= mask[cb][i + 1] << (64 - s);
+            seen |= bits & low(end - t) & ~low(base - t);
+        }
+        return seen;
+    }
+};
+// The lane's 16 of a page's tokens: bit k is token 16 (k / 4) + 4 g + k % 4.
+__device__ __forceinline__ uint32_t lane_bits(uint64_t page, int g) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r |= ((uint32_t)(page >> (16 * j + 4 * g)) & 15u) << (4 * j);
+    return r;
+}
 
 // 2^n for the n of units and scales; below the normal numbers 0.
 __device__ __forceinline__ float power_of_two(int n) {
@@ -353,8 +387,8 @@ __device__ __forceinline__ void move_unit(AttState<D, CB>& st, int unit) {
 // One page.  kf(j, k): the lane's 8 elements of K of token tile j and step k of
 // the contraction; vf(i, u): its 8 tokens of V of 16-element tile i and step u,
 // in units of 2^st.unit.
-template <int D, int CB, class KF, class VF>
-__device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<CB>& cols,
+template <int D, int CB, bool MASKED, class KF, class VF>
+__device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<CB, MASKED>& cols,
                                             const bf16x8 (&q)[CB][D / 32], KF kf, VF vf, uint32_t ks,
                                             uint32_t vs, int base, float c0) {
     constexpr int VI = D / 16;
@@ -395,11 +429,17 @@ __device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<C
         for (int cb = 0; cb < CB; ++cb) {
             seen[cb] = 0;
             top[cb] = -INFINITY;
+            if constexpr (MASKED) seen[cb] = lane_bits(cols.page(cb, base), g);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                const int t = base + 16 * (k / 4) + 4 * g + k % 4;
-                const bool in = t >= cols.first[cb] && t <= cols.last[cb];
-                seen[cb] |= in ? 1u << k : 0u;
+                bool in;
+                if constexpr (MASKED) {
+                    in = (seen[cb] >> k) & 1u;
+                } else {
+                    const int t = base + 16 * (k / 4) + 4 * g + k % 4;
+                    in = t >= cols.first[cb] && t <= cols.last[cb];
+                    seen[cb] |= in ? 1u << k : 0u;
+                }
                 top[cb] = fmaxf(top[cb], in ? s[cb][k / 4][k % 4] : -INFINITY);
             }
         }
@@ -476,9 +516,19 @@ __device__ __forceinline__ Column column(const AttendArgs& a, const Seq& sq, int
     return r;
 }
 
-template <int D, int CB>
+// The rows of its sequence that a tree's row sees.
+__device__ __forceinline__ int rows_seen(const AttendArgs& a, const Seq& sq, const uint64_t* mask) {
+    int c = 0;
+    for (int i = 0; i < a.mask_words && 64 * i < sq.n; ++i) {
+        const int left = sq.n - 64 * i;
+        c += __popcll(mask[i] & (left >= 64 ? ~0ull : (1ull << left) - 1));
+    }
+    return c;
+}
+
+template <int D, int CB, bool MASKED>
 __device__ __forceinline__ void load_q(const AttendArgs& a, const Seq& sq, int kvh, int c0, int cols,
-                                       bf16x8 (&q)[CB][D / 32], Columns<CB>& v) {
+                                       bf16x8 (&q)[CB][D / 32], Columns<CB, MASKED>& v) {
     const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;   // scores take |scale|
 #pragma unroll
@@ -487,6 +537,12 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const Seq& sq, int k
         const Column k = column(a, sq, c < cols ? c : cols - 1);
         v.first[cb] = k.first;
         v.last[cb] = k.last;
+        if constexpr (MASKED) {
+            v.mask[cb] = a.masks ? a.masks + (sq.lo + k.i) * a.mask_words : nullptr;
+            if (a.masks)
+                v.first[cb] = a.window > 0
+                    ? (int)max((int64_t)0, (int64_t)sq.L - sq.n - a.window + rows_seen(a, sq, v.mask[cb])) : 0;
+        }
         const uint16_t* src = a.q + (sq.lo + k.i) * a.ldq + (int64_t)(kvh * a.group + k.head) * D;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
@@ -498,15 +554,62 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const Seq& sq, int k
     const int ce = min(c0 + 16 * CB, cols) - 1;
     v.all_to = column(a, sq, c0).last;
     v.all_from = column(a, sq, ce).first;
+    if constexpr (MASKED) {
+        v.words = a.mask_words;
+        v.base = sq.L - sq.n;
+        v.end = sq.L;
+        v.sinks = a.sinks;
+        if (a.masks) {               // a row sees at most n rows
+            v.all_to = v.base - 1;
+            v.all_from = a.window > 0 ? (int)max((int64_t)0, (int64_t)sq.L - a.window) : 0;
+        }
+    }
 }
 
-// The tokens' pages [p0, p1) that columns [c0, ce] see.
+// Pages are walked by places: with sinks, a run of the first pages and then, past a gap, those
+// of the window.  Without, a place is a page's number.
+template <bool MASKED>
+struct Places {
+    static constexpr int sinks = 0;
+    __device__ __forceinline__ int page(int p) const { return p; }
+};
+template <>
+struct Places<true> {
+    int sinks = 0, gap = 0;          // pages before the gap, and in it
+    __device__ __forceinline__ int page(int p) const { return p < sinks ? p : p + gap; }
+};
+
+// The tokens' pages [p0, p1) that columns [c0, ce] see, beside the sinks.
+template <bool MASKED>
 __device__ __forceinline__ void page_range(const AttendArgs& a, const Seq& sq, int c0, int ce,
                                            int& p0, int& p1) {
-    const int first = column(a, sq, c0).first, last = column(a, sq, ce).last;
+    int first = column(a, sq, c0).first, last = column(a, sq, ce).last;
+    if constexpr (MASKED) {
+        if (a.masks) {               // a row that sees no row of its own looks back the furthest
+            first = a.window > 0 ? (int)max((int64_t)0, (int64_t)sq.L - sq.n - a.window) : 0;
+            last = sq.L - 1;
+        }
+    }
     p0 = first / kKvPage;
     p1 = last < 0 ? 0 : min(last / kKvPage + 1, a.seqs.max_pages);
     if (p1 < p0) p1 = p0;
+}
+
+// The places [p0, p1) of them, from 0 on where there are sinks.
+template <bool MASKED>
+__device__ __forceinline__ Places<MASKED> place_range(const AttendArgs& a, const Seq& sq, int c0,
+                                                      int ce, int& p0, int& p1) {
+    Places<MASKED> r;
+    page_range<MASKED>(a, sq, c0, ce, p0, p1);
+    if constexpr (MASKED) {
+        if (p1 > p0) {
+            r.sinks = min((int)(((int64_t)a.sinks + kKvPage - 1) / kKvPage), p0);
+            r.gap = p0 - r.sinks;
+            p1 -= r.gap;
+            p0 = 0;
+        }
+    }
+    return r;
 }
 
 // A split's part of them: runs of split_pages pages; the last split takes what is left,
@@ -560,7 +663,7 @@ __device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq,
 // (6.0 TB/s; a call 115, without ONCE 131).  Sequences that share their pages pay
 // for it, as the host does not know of them: 64 forks of one such prompt take 78 us
 // a call and would take 61, 8 of 100000 tokens 246 and 222 (apart 183 and 205).
-template <int D, int W, bool ONCE>
+template <int D, int W, bool ONCE, bool MASKED>
 __global__ void __launch_bounds__(64 * W, D == 256 ? 1 : W == 4 ? 3 : 2)
 attend_split_kernel(const AttendArgs a) {
     __shared__ float sm[W][16], sl[W][16];
@@ -578,14 +681,14 @@ attend_split_kernel(const AttendArgs a) {
     const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int p0, p1;
-    page_range(a, sq, c0, min(c0 + 16, cols) - 1, p0, p1);
+    const Places<MASKED> places = place_range<MASKED>(a, sq, c0, min(c0 + 16, cols) - 1, p0, p1);
     int from = p0, to = p1;
     split_range(a, split, from, to);
     if (split > 0 && from >= to) return;           // nor does the join look at it
     const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
-    int32_t next = from + wave < to ? row[from + wave] : 0;
+    int32_t next = from + wave < to ? row[places.page(from + wave)] : 0;
     bf16x8 q[1][D / 32];
-    Columns<1> v;
+    Columns<1, MASKED> v;
     load_q<D, 1>(a, sq, kvh, c0, cols, q, v);
 
     AttState<D, 1> st;
@@ -593,9 +696,10 @@ attend_split_kernel(const AttendArgs a) {
     Unit unit;
     const float cc = __builtin_fabsf(a.scale) * kLog2e;
     const int64_t head_off = (int64_t)kvh * D * kKvPage;
-    for (int p = from + wave; p < to; p += W) {
+    for (int at_ = from + wave; at_ < to; at_ += W) {
+        const int p = places.page(at_);
         const int32_t page = next;
-        next = p + W < to ? row[p + W] : 0;        // ahead of this page's loads
+        next = at_ + W < to ? row[places.page(at_ + W)] : 0;   // ahead of this page's loads
         if (page < 0 || page >= a.cache.num_pages) continue;
         const int64_t at = (int64_t)page * a.cache.page_stride + head_off;
         const uint8_t* kb = a.cache.k_codes + at + g * 1024 + r * 16;
@@ -623,7 +727,7 @@ attend_split_kernel(const AttendArgs a) {
                 for (int j = 0; j < 4; ++j)
                     vr[i][j] &= before_end(p * kKvPage + 16 * j + 4 * g, sq.L);
         }
-        attend_page<D, 1>(
+        attend_page<D, 1, MASKED>(
             st, v, q,
             [&](int j, int k) {
                 const u32x4& x = kr[j][k / 2];
@@ -678,7 +782,7 @@ attend_split_kernel(const AttendArgs a) {
 // write as many (each wave's 1 KiB of V is dealt to its lanes by columns).  Bound
 // by the vector instructions of the softmax beside the matrix cores: 2 x 2048
 // rows in 8192 tokens, 32 heads of 128, reach 1.06 PFLOP/s (339 us).
-template <int D, int CB, int W>
+template <int D, int CB, int W, bool MASKED>
 __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs a) {
     constexpr int kHalf = D * kKvPage, kT = 64 * W, kLoads = kHalf / (kT * 16);
     __shared__ bf16x8 k0[kHalf / 8], k1[kHalf / 8];
@@ -699,11 +803,12 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
     const int c0 = w0 + 16 * CB * wave;
     const bool mine = c0 < cols;
     bf16x8 q[CB][D / 32];
-    Columns<CB> v;
+    Columns<CB, MASKED> v;
     load_q<D, CB>(a, sq, kvh, mine ? c0 : w0, cols, q, v);
-    int p0, p1, q0 = 0, q1 = 0;                    // the workgroup's pages, the wave's
-    page_range(a, sq, w0, min(w0 + 16 * CB * W, cols) - 1, p0, p1);
-    if (mine) page_range(a, sq, c0, min(c0 + 16 * CB, cols) - 1, q0, q1);
+    int p0, p1, q0 = 0, q1 = 0;                    // the workgroup's places, the wave's pages
+    const Places<MASKED> places =
+        place_range<MASKED>(a, sq, w0, min(w0 + 16 * CB * W, cols) - 1, p0, p1);
+    if (mine) page_range<MASKED>(a, sq, c0, min(c0 + 16 * CB, cols) - 1, q0, q1);
     if (a.splits > 1) {
         split_range(a, split, p0, p1);
         if (split > 0 && p0 >= p1) return;         // nor does the join look at it
@@ -724,7 +829,7 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
     int page_in = -1;                              // the page fetched last; -1: none
     int lane0 = 0;
     asm volatile("" : "+v"(lane0));
-    auto look_up = [&](int p) { page_v = row[min(p, p1 - 1) + lane0]; };
+    auto look_up = [&](int p) { page_v = row[places.page(min(p, p1 - 1)) + lane0]; };
     auto fetch = [&](int p) {
         const int page = __builtin_amdgcn_readfirstlane(page_v);
         page_in = p < p1 && page >= 0 && page < a.cache.num_pages ? page : -1;
@@ -749,12 +854,13 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
         ks = __builtin_amdgcn_readfirstlane(ks_v);
         vs = __builtin_amdgcn_readfirstlane(vs_v);
         const float vf = unit.follow(vs);
-        if (p * kKvPage + kKvPage > sq.L) {
+        const int page = places.page(p);
+        if (page * kKvPage + kKvPage > sq.L) {
 #pragma unroll
             for (int k = 0; k < kLoads; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    vr[k][j] &= before_end(p * kKvPage + 16 * j + 4 * g, sq.L);
+                    vr[k][j] &= before_end(page * kKvPage + 16 * j + 4 * g, sq.L);
         }
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
@@ -779,11 +885,15 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
         convert(p + 1, ko, vo);
         fetch(p + 2);
         if (unit_now != st.unit) move_unit(st, unit_now);
-        if (p < q0 || p >= q1 || ks_now == 256u) return;
-        attend_page<D, CB>(
+        const int page = places.page(p);
+        bool skip = page < q0 || page >= q1;
+        if constexpr (MASKED)        // the workgroup's first columns look back further
+            if (mine && page < q1 && (int64_t)page * kKvPage < a.sinks) skip = false;
+        if (skip || ks_now == 256u) return;
+        attend_page<D, CB, MASKED>(
             st, v, q, [&](int j, int k) { return kb[(8 * (k >> 1) + 2 * g + (k & 1)) * 64 + 16 * j + r]; },
             [&](int i, int u) { return vb[(2 * g + u) * D + (16 * i + r)]; }, ks_now,
-            vs_now, p * kKvPage, cc);
+            vs_now, page * kKvPage, cc);
     };
     for (int p = p0; p < p1; p += 2) {
         page_step(p, k0, v0, k1, v1);
@@ -805,7 +915,7 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
 // order.  The weights of 64 splits are found at once, a lane each, while the first sums are on
 // their way.  Both sides of kJoinAlone: 64 rows of 32 heads of 128, few splits each, take 4.7 us
 // with a wave for a pair and 8.6 with four; 4 rows of 32 heads over 32 splits 12.0 and 6.3.
-template <int D, int W>
+template <int D, int W, bool MASKED>
 __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a) {
     constexpr int E = D / 64, kAhead = 8;
     __shared__ float so[kWaves][D], sl[kWaves];
@@ -822,7 +932,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
     // splits past the sequence's pages hold nothing and are not read
     const int c0 = (i * a.group + head % a.group) / a.block_cols * a.block_cols;
     int p0, p1;
-    page_range(a, sq, c0, min(c0 + a.block_cols, columns(a, sq)) - 1, p0, p1);
+    place_range<MASKED>(a, sq, c0, min(c0 + a.block_cols, columns(a, sq)) - 1, p0, p1);
     const int used = (int)min((int64_t)a.splits,
                               ((int64_t)p1 - p0 + a.split_pages - 1) / a.split_pages);
     const int64_t row = sq.lo + i, at = row * a.num_q_heads + head;
@@ -904,35 +1014,35 @@ constexpr int kRowColumns = 128, kWideColumns = 256;
 
 constexpr int64_t kJoinAlone = 1024;
 
-template <int D, int W>
+template <int D, int W, bool MASKED>
 void attend_rows(const AttendArgs& a, dim3 grid, hipStream_t stream) {
-    hipLaunchKernelGGL((attend_rows_kernel<D, kRowBlocks<D>, W>), grid, dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((attend_rows_kernel<D, kRowBlocks<D>, W, MASKED>), grid, dim3(64 * W), 0, stream, a);
 }
 
-template <int D>
+template <int D, bool MASKED>
 void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
     const int64_t per = (int64_t)a.seqs.num_seqs * a.cache.num_heads * a.col_blocks;
     const dim3 grid((uint32_t)(per * a.splits));
     if (p.rows_form) {
-        if constexpr (D == 256) attend_rows<D, 8>(a, grid, stream);
-        else if constexpr (D == 64) attend_rows<D, 4>(a, grid, stream);
-        else if (p.wide) attend_rows<D, 8>(a, grid, stream);
-        else attend_rows<D, 4>(a, grid, stream);
+        if constexpr (D == 256) attend_rows<D, 8, MASKED>(a, grid, stream);
+        else if constexpr (D == 64) attend_rows<D, 4, MASKED>(a, grid, stream);
+        else if (p.wide) attend_rows<D, 8, MASKED>(a, grid, stream);
+        else attend_rows<D, 4, MASKED>(a, grid, stream);
     } else if (p.wide) {
-        hipLaunchKernelGGL((attend_split_kernel<D, 8, false>), grid, dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((attend_split_kernel<D, 8, false, MASKED>), grid, dim3(512), 0, stream, a);
     } else if (a.col_blocks == 1) {
-        hipLaunchKernelGGL((attend_split_kernel<D, 4, true>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attend_split_kernel<D, 4, true, MASKED>), grid, dim3(256), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((attend_split_kernel<D, 4, false>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attend_split_kernel<D, 4, false, MASKED>), grid, dim3(256), 0, stream, a);
     }
     if (a.splits > 1) {
         const int64_t pairs = (int64_t)a.seqs.num_seqs * a.max_q * a.num_q_heads;
         if (pairs >= kJoinAlone)
-            hipLaunchKernelGGL((attend_join_kernel<D, 1>),
+            hipLaunchKernelGGL((attend_join_kernel<D, 1, MASKED>),
                                dim3((uint32_t)((pairs + kWaves - 1) / kWaves)), dim3(kThreads), 0,
                                stream, a);
         else
-            hipLaunchKernelGGL((attend_join_kernel<D, kWaves>), dim3((uint32_t)pairs),
+            hipLaunchKernelGGL((attend_join_kernel<D, kWaves, MASKED>), dim3((uint32_t)pairs),
                                dim3(kThreads), 0, stream, a);
     }
 }
@@ -968,12 +1078,15 @@ constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40;
 constexpr int64_t kRowsLeast = 4;
 
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
-                       int64_t max_q, int64_t max_kv, int64_t window) {
+                       int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks) {
     const int64_t cols = max_q * (num_q_heads / num_heads);
     AttendPlan p{};
     p.rows_form = cols > 64;
     int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
-    if (window > 0 && window < max_kv) pages = (window + max_q) / kKvPage + 2;
+    if (window > 0 && window < max_kv) {
+        const int64_t seen = (window + max_q) / kKvPage + 2 + (sinks + kKvPage - 1) / kKvPage;
+        pages = sinks > 0 ? std::min(pages, seen) : seen;
+    }
     const double heads = (double)num_seqs * (double)num_heads;
     p.block_cols = p.rows_form ? kRowColumns : 16;
     if (p.rows_form) {
@@ -1011,12 +1124,20 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     return p;
 }
 
-hipError_t launch_kv_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+namespace {
+template <bool MASKED>
+void attend_of(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
     switch (a.cache.head_dim) {
-        case 64: attend<64>(a, p, stream); break;
-        case 128: attend<128>(a, p, stream); break;
-        default: attend<256>(a, p, stream); break;
+        case 64: attend<64, MASKED>(a, p, stream); break;
+        case 128: attend<128, MASKED>(a, p, stream); break;
+        default: attend<256, MASKED>(a, p, stream); break;
     }
+}
+}  // namespace
+
+hipError_t launch_kv_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+    if (a.masks || (a.sinks > 0 && a.window > 0)) attend_of<true>(a, p, stream);
+    else attend_of<false>(a, p, stream);
     return hipGetLastError();
 }
 

@@ -128,7 +128,7 @@ int check_seqs(const uint32_t* row_offsets, const int32_t* kv_lens, const int32_
 
 // The query heads and sizes of an attention call, and how its work is cut.
 int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs, int64_t max_q,
-         int64_t max_kv, int64_t window, bsq::AttendPlan* p) {
+         int64_t max_kv, int64_t window, int64_t sinks, bsq::AttendPlan* p) {
     if (num_heads < 1 || num_q_heads < 1 || num_q_heads > 65535 || num_q_heads % num_heads != 0)
         return fail(BSQ_ERR_INVALID_ARG,
                     "num_q_heads=%lld must be in 1 .. 65535 and a multiple of num_heads=%lld",
@@ -149,7 +149,7 @@ int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_s
         *p = bsq::AttendPlan{};
         return BSQ_OK;
     }
-    *p = bsq::plan_attend(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window);
+    *p = bsq::plan_attend(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks);
     const double blocks = (double)num_seqs * (double)num_heads * (double)p->col_blocks * p->splits;
     const double pairs = (double)num_seqs * (double)max_q * (double)num_q_heads;
     // the join has at least a wave for each pair
@@ -225,12 +225,21 @@ int kv_cache_append(const bsq_kv_cache* cache, const void* k, int64_t ldk, const
 int64_t kv_cache_attention_workspace(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
                                      int64_t num_seqs, int64_t num_rows, int64_t max_q,
                                      int64_t max_kv, int64_t window) {
+    return kv_cache_attention_masked_workspace(num_heads, head_dim, num_q_heads, num_seqs, num_rows,
+                                               max_q, max_kv, window, 0);
+}
+
+int64_t kv_cache_attention_masked_workspace(int64_t num_heads, int64_t head_dim,
+                                            int64_t num_q_heads, int64_t num_seqs,
+                                            int64_t num_rows, int64_t max_q, int64_t max_kv,
+                                            int64_t window, int64_t sinks) {
     bsq::AttendPlan p;
-    if (num_rows < 0 || num_rows > kMaxInt) {
-        fail(BSQ_ERR_INVALID_ARG, "num_rows=%lld must be in 0 .. 2^31 - 1", (long long)num_rows);
+    if (num_rows < 0 || num_rows > kMaxInt || sinks < 0 || sinks > kMaxInt) {
+        fail(BSQ_ERR_INVALID_ARG, "num_rows=%lld and sinks=%lld must be in 0 .. 2^31 - 1",
+             (long long)num_rows, (long long)sinks);
         return -1;
     }
-    if (plan(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, &p) != BSQ_OK)
+    if (plan(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks, &p) != BSQ_OK)
         return -1;
     ok();
     return attend_workspace(p, num_rows, num_q_heads, head_dim);
@@ -242,14 +251,34 @@ int kv_cache_attention(const bsq_kv_cache* cache, const void* q, int64_t ldq, in
                        int64_t num_seqs, int64_t num_rows, int64_t max_q, int64_t max_kv,
                        float scale, int64_t window, void* out, int64_t ldo, float* lse,
                        void* workspace, int64_t workspace_bytes, void* stream) {
+    return kv_cache_attention_masked(cache, q, ldq, num_q_heads, row_offsets, kv_lens, block_table,
+                                     table_stride, max_pages, num_seqs, num_rows, max_q, max_kv,
+                                     scale, window, 0, nullptr, 0, out, ldo, lse, workspace,
+                                     workspace_bytes, stream);
+}
+
+int kv_cache_attention_masked(const bsq_kv_cache* cache, const void* q, int64_t ldq,
+                              int64_t num_q_heads, const uint32_t* row_offsets,
+                              const int32_t* kv_lens, const int32_t* block_table,
+                              int64_t table_stride, int64_t max_pages, int64_t num_seqs,
+                              int64_t num_rows, int64_t max_q, int64_t max_kv, float scale,
+                              int64_t window, int64_t sinks, const uint64_t* masks,
+                              int64_t mask_words, void* out, int64_t ldo, float* lse,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
     bsq::AttendArgs a{};
     bsq::AttendPlan p;
     int st = check_cache(cache, &a.cache);
     if (st == BSQ_OK)
         st = check_seqs(row_offsets, kv_lens, block_table, table_stride, max_pages, num_seqs,
                         num_rows, max_q, &a.seqs);
-    if (st == BSQ_OK)
-        st = plan(cache->num_heads, cache->head_dim, num_q_heads, num_seqs, max_q, max_kv, window, &p);
+    if (st != BSQ_OK) return st;
+    if (sinks < 0 || sinks > kMaxInt)
+        return fail(BSQ_ERR_INVALID_ARG, "sinks=%lld must be in 0 .. 2^31 - 1", (long long)sinks);
+    if (masks && (mask_words < 0 || mask_words > kMaxInt || 64 * mask_words < max_q))
+        return fail(BSQ_ERR_INVALID_ARG, "mask_words=%lld must hold max_q=%lld bits",
+                    (long long)mask_words, (long long)max_q);
+    if (masks && !aligned(masks, 8)) return fail(BSQ_ERR_INVALID_ARG, "masks must be 8-byte aligned");
+    st = plan(cache->num_heads, cache->head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks, &p);
     if (st != BSQ_OK) return st;
     if (!std::isfinite(scale)) return fail(BSQ_ERR_INVALID_ARG, "scale must be finite");
     if (num_seqs == 0 || num_rows == 0 || max_q == 0) return ok();
@@ -270,6 +299,9 @@ int kv_cache_attention(const bsq_kv_cache* cache, const void* q, int64_t ldq, in
     if (need > 0)
         a.part_ml = a.part_o + (int64_t)p.splits * num_rows * num_q_heads * cache->head_dim;
     a.window = window > kMaxInt ? 0 : window;      // longer than any sequence; its places stay in 64 bits
+    a.masks = masks;
+    a.mask_words = masks ? (int32_t)mask_words : 0;
+    a.sinks = (int32_t)sinks;
     a.scale = scale;
     a.num_q_heads = (int32_t)num_q_heads;
     a.group = (int32_t)(num_q_heads / cache->num_heads);

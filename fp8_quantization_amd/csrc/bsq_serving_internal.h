@@ -56,6 +56,8 @@ struct AttendArgs {
     float* part_o;                   // [splits][num_rows][num_q_heads][head_dim]
     float* part_ml;                  // [splits][num_rows][num_q_heads][2]
     int64_t window;                  // 0: none
+    const uint64_t* masks;           // nullable; [num_rows][mask_words]
+    int32_t mask_words, sinks;       // sinks: of account with a window alone
     float scale;
     int32_t num_q_heads;
     int32_t group;                   // num_q_heads / num_heads
@@ -76,7 +78,7 @@ struct AttendPlan {
     int32_t threads;                 // of a workgroup
 };
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
-                       int64_t max_q, int64_t max_kv, int64_t window);
+                       int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks);
 hipError_t launch_kv_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
 
 struct PageArgs {

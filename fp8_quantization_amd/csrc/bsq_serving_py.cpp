@@ -316,7 +316,7 @@ PyObject* append(Args& a) {
 }
 
 // q, cache, row_offsets, block_table, kv_lens, max_q, max_kv, scale, window, out, lse, want_lse,
-// workspace, stream -> (out, lse or None)
+// workspace, sinks, masks, stream -> (out, lse or None)
 PyObject* attention(Args& a) {
     const at::Tensor& q = rows_of(a.tensor("q"), "q", 3);
     const bsq_kv_cache c = cache_of(a);
@@ -329,6 +329,8 @@ PyObject* attention(Args& a) {
     const at::Tensor* lse = a.tensor("lse", true);
     const bool want_lse = a.integer("return_lse") != 0;
     const at::Tensor* given = a.tensor("workspace", true);
+    const int64_t sinks = a.integer("sinks");
+    const at::Tensor* masks = a.tensor("masks", true);
     const CallStream stream(a);
     const int64_t R = q.size(0), Hq = q.size(1), D = q.size(2);
     if (D != c.head_dim)
@@ -350,15 +352,26 @@ PyObject* attention(Args& a) {
         new_lse = empty({R, Hq}, at::kFloat, *a.device);
         lse = &new_lse;
     }
-    const int64_t need = size_of(kv_cache_attention_workspace(c.num_heads, D, Hq, t.seqs, R, max_q,
-                                                              max_kv, window));
+    if (masks) {
+        const bool wide = masks->scalar_type() == at::kLong || masks->scalar_type() == at::kUInt64;
+        if (!wide || masks->dim() != 2 || !masks->is_contiguous())
+            refuse(0, "masks must be a contiguous 2-D GPU tensor of dtype int64 or uint64");
+        if (masks->size(0) < R)
+            refuse(BSQ_ERR_INVALID_ARG, "masks has %lld rows; it must have %lld",
+                   (long long)masks->size(0), (long long)R);
+        if (64 * masks->size(1) < max_q)   // none has no address, which would mean no masks
+            refuse(BSQ_ERR_INVALID_ARG, "masks has %lld words a row; it must hold max_q=%lld bits",
+                   (long long)masks->size(1), (long long)max_q);
+    }
+    const int64_t need = size_of(kv_cache_attention_masked_workspace(
+        c.num_heads, D, Hq, t.seqs, R, max_q, max_kv, window, sinks));
     const Workspace ws(a, need ? given : nullptr, need);
-    check(kv_cache_attention(&c, q.data_ptr(), row_stride(q), Hq,
-                             static_cast<uint32_t*>(offsets->data_ptr()), t.lens, t.p, t.stride,
-                             t.pages, t.seqs, R, max_q, max_kv, (float)scale, window,
-                             out->data_ptr(), row_stride(*out),
-                             lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.p, ws.bytes,
-                             stream.raw));
+    check(kv_cache_attention_masked(
+        &c, q.data_ptr(), row_stride(q), Hq, static_cast<uint32_t*>(offsets->data_ptr()), t.lens, t.p,
+        t.stride, t.pages, t.seqs, R, max_q, max_kv, (float)scale, window, sinks,
+        masks ? static_cast<uint64_t*>(masks->data_ptr()) : nullptr, masks ? masks->size(1) : 0,
+        out->data_ptr(), row_stride(*out), lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.p,
+        ws.bytes, stream.raw));
     PyObject* o = stream.give(*out, new_out);
     PyObject* l = lse ? stream.give(*lse, new_lse) : none();
     PyObject* r = o && l ? PyTuple_Pack(2, o, l) : nullptr;

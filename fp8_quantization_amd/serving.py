@@ -48,6 +48,9 @@ for _name, _res, *_args in (
         ("moe_few_tokens", _i32, _i32, _p, *[_i64] * 6, _p, _p, _p, _p, _p, _i32, _p, _p, _p, _i64,
          _p, _i64, _p),
         ("moe_few_tokens_workspace", _i64, *[_i64] * 4),
+        ("kv_cache_attention_masked", _i32, _p, _p, _i64, _i64, _p, _p, _p, *[_i64] * 6, _f32, _i64,
+         _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p),
+        ("kv_cache_attention_masked_workspace", _i64, *[_i64] * 9),
         ("qk_norm_rope", _i32, _i32, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _p, _p,
          _f32, _p, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _i64, _p),
         ("bsq_serving_last_error", ctypes.c_char_p)):
@@ -110,7 +113,7 @@ def kv_cache_attention(q: torch.Tensor, cache: KvCache, row_offsets: torch.Tenso
     sequence owns are left as they were."""
     r = _serving.attention(q, cache, row_offsets, block_table, kv_lens, max_q, max_kv,
                            q.shape[-1] ** -0.5 if scale is None else scale, window, out, lse,
-                           return_lse, workspace, stream)
+                           return_lse, workspace, 0, None, stream)
     return r if return_lse else r[0]
 
 
@@ -187,3 +190,20 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
     output may be its BF16 input itself."""
     return _serving.rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out,
                          k_out, v_out, stream)
+
+
+def kv_cache_attention_masked(q: torch.Tensor, cache: KvCache, row_offsets: torch.Tensor,
+                              kv_lens: torch.Tensor, block_table: torch.Tensor, max_q: int,
+                              max_kv: int, masks=None, sinks: int = 0, scale: float | None = None,
+                              window: int = 0, out=None, return_lse: bool = False, lse=None,
+                              workspace=None, stream=None):
+    """``kv_cache_attention`` with two more masks.  ``sinks``: with a window,
+    that many first tokens of a sequence stay visible.  ``masks`` (int64 or
+    uint64 [rows, words]): the rows are nodes of a tree of drafted tokens, and
+    a row sees those rows of its sequence whose bits (x % 64 of word x / 64)
+    are set, itself only if its own is, beside the tokens before them; a window
+    counts the rows seen.  All else as there."""
+    r = _serving.attention(q, cache, row_offsets, block_table, kv_lens, max_q, max_kv,
+                           q.shape[-1] ** -0.5 if scale is None else scale, window, out, lse,
+                           return_lse, workspace, sinks, masks, stream)
+    return r if return_lse else r[0]

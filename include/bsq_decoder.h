@@ -59,6 +59,43 @@ int qk_norm_rope(int dtype, const void* q, int64_t ldq, int64_t num_q_heads, con
                  int interleaved, void* q_out, int64_t ldqo, void* k_out, int64_t ldko, void* v_out,
                  int64_t ldvo, void* stream);
 
+/*
+ * kv_cache_attention (bsq_serving.h) with two more masks.  Of a sequence with
+ * n rows and L tokens, the rows being its last tokens, base = L - n tokens
+ * lie before them.
+ *
+ * masks NULL: row i is at place P = base + i and sees the tokens j <= P with
+ *     j > P - window or j < sinks   (window 0: all of them).
+ * masks given: the rows are nodes of a tree of drafted tokens.  Row i sees
+ *     the rows (token base + x) whose bit x is set in its mask, bit x % 64 of
+ *     word x / 64, itself only if its own is; and of the tokens before them
+ *     j >= base - (window - c) or j < sinks   (window 0: all of them), where c
+ *     is the number of rows it sees: base + c - 1 is then the place of the
+ *     last node of a path of c.  Bits from n on are ignored.
+ *
+ *   masks         uint64 [num_rows][mask_words] without gaps, 8-byte aligned, or
+ *                 NULL.  max_q is at most 64 * mask_words.
+ *   window        0, or the number of tokens seen beside the sinks.
+ *   sinks         first tokens that stay visible, 0 .. 2^31 - 1.
+ * Pages of which no row sees a token are not read, and neither are their
+ * table entries.  All else as for kv_cache_attention: rows that see nothing,
+ * NaN scales, pages outside the cache, sums and their order, and the
+ * workspace, of kv_cache_attention_masked_workspace(...) bytes (-1 for sizes
+ * that the call would refuse).
+ */
+int kv_cache_attention_masked(const bsq_kv_cache* cache, const void* q, int64_t ldq,
+                              int64_t num_q_heads, const uint32_t* row_offsets,
+                              const int32_t* kv_lens, const int32_t* block_table,
+                              int64_t table_stride, int64_t max_pages, int64_t num_seqs,
+                              int64_t num_rows, int64_t max_q, int64_t max_kv, float scale,
+                              int64_t window, int64_t sinks, const uint64_t* masks,
+                              int64_t mask_words, void* out, int64_t ldo, float* lse,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+int64_t kv_cache_attention_masked_workspace(int64_t num_heads, int64_t head_dim,
+                                            int64_t num_q_heads, int64_t num_seqs,
+                                            int64_t num_rows, int64_t max_q, int64_t max_kv,
+                                            int64_t window, int64_t sinks);
+
 #ifdef __cplusplus
 }
 #endif

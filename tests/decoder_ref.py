@@ -32,3 +32,85 @@ def norm_rope(x, weight, eps, positions, inv_freq, interleaved):
     both = (np.abs(y[..., p]) + np.abs(y[..., r])) * (18 * U + np.abs(angle)[:, None] * 2.0 ** -50)
     size[..., p] = size[..., r] = both
     return out, np.abs(out) * BF16 + size * (1 + BF16) + 2.0 ** -133
+
+
+# ------------------------------------------------------------------ attention under masks
+
+
+def seen_tokens(L, n, i, window, sinks, mask):
+    """The tokens that row i of n rows and L tokens sees; mask: the rows it sees, or None."""
+    base, j = L - n, np.arange(max(L, 0))
+    if mask is None:
+        near = (j > base + i - window) | (j < sinks) if window else j >= 0
+        return near & (j <= base + i)
+    near = (j >= base - (window - len(mask))) | (j < sinks) if window else j >= 0
+    return near & (j < base) | np.isin(j, base + np.array(sorted(mask), int))
+
+
+def attention(cache, q, offsets, lens, table, scale, window=0, sinks=0, masks=None):
+    """kv_cache_attention_masked with serving_ref.attention's outputs and bounds, whose terms it
+    shares; masks: for each row a set of the rows of its sequence that it sees."""
+    rows, hq, D = q.shape
+    heads = cache.ks.shape[1]
+    out, lse = np.zeros((rows, hq, D)), np.full((rows, hq), -np.inf)
+    bo, bl = np.zeros((rows, hq, D)), np.zeros((rows, hq))
+    owned = np.zeros(rows, bool)
+    for s, L in enumerate(lens):
+        lo, hi = int(offsets[s]), int(offsets[s + 1])
+        n = hi - lo
+        owned[lo:hi] = True
+        there = np.zeros(max(L, 0), bool)
+        for p in range((L + 63) // 64):
+            page = int(table[s][p]) if p < len(table[s]) else -1
+            there[64 * p:64 * p + 64] = 0 <= page < cache.ks.shape[0]
+        see = [seen_tokens(L, n, i, window, sinks, None if masks is None else
+                           {x for x in masks[lo + i] if x < n}) & there for i in range(n)]
+        some = np.any(see, 0) if n else there & False
+        for h in range(heads):
+            k, v = np.zeros((max(L, 0), D)), np.zeros((max(L, 0), D))
+            for p in np.unique(np.nonzero(some)[0] // 64):
+                m = min(64, L - 64 * p)
+                k[64 * p:64 * p + m] = cache.values("k", int(table[s][p]), h, m)
+                v[64 * p:64 * p + m] = cache.values("v", int(table[s][p]), h, m)
+            for i in range(n):
+                if not see[i].any():
+                    continue
+                K, V = k[see[i]], v[see[i]]
+                for col in range(h * (hq // heads), (h + 1) * (hq // heads)):
+                    x = q[lo + i, col]
+                    z = scale * (K @ x)
+                    bad = np.isnan(z).any() or np.isnan(V).any()
+                    if bad:
+                        out[lo + i, col] = lse[lo + i, col] = np.nan
+                        continue
+                    m = z.max()
+                    w = np.exp(z - m)
+                    l = w.sum()
+                    out[lo + i, col], lse[lo + i, col] = w @ V / l, m + np.log(l)
+                    ds = abs(scale) * (D + 4) * U * (np.abs(K) @ np.abs(x)).max() + \
+                        (np.abs(z).max() + 16) * 2.0 ** -22 + 2.0 ** -21
+                    cnt = (len(K) + 64) * U
+                    tiny = 2.0 ** -36 * np.abs(V).sum(0) / l
+                    bo[lo + i, col] = np.abs(out[lo + i, col]) * BF16 + tiny + 2.0 ** -133 + \
+                        w @ np.abs(V) / l * (2.0 ** -11 + 2 * ds + 2 * cnt) * (1 + 2.0 ** -7)
+                    bl[lo + i, col] = ds + cnt + abs(lse[lo + i, col]) * 2.0 ** -22 + 2.0 ** -20
+    return out, lse, bo, bl, owned
+
+
+def words(masks, n):
+    """Sets as int64 [rows, n] words of 64 bits."""
+    w = np.zeros((len(masks), n), np.uint64)
+    for r, m in enumerate(masks):
+        for x in m:
+            if x < 64 * n:
+                w[r, x // 64] |= np.uint64(1 << (x % 64))
+    return w.view(np.int64)
+
+
+def random_tree(rng, n, most_back=6):
+    """For each node the set of its ancestors and itself."""
+    masks = []
+    for i in range(n):
+        parent = i - int(rng.integers(1, most_back + 1))
+        masks.append((masks[parent] if parent >= 0 else set()) | {i})
+    return masks

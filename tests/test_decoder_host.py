@@ -70,3 +70,72 @@ def test_reference_rotation_keeps_lengths_and_differences():
         assert not np.allclose(a, b) and np.array_equal(a[..., 16:], x[..., 16:])
     n, bound = R.norm_rope(x, np.ones(32), 0.0, np.zeros(4, int), f, False)
     assert np.allclose((n * n).mean(-1), 1) and np.all(bound < 0.02)
+
+
+# ------------------------------------------------------------------ attention under masks
+
+
+def masked(lib, sinks=0, masks=FAKE, words=1, max_q=1, window=0, ws=FAKE, ws_bytes=1 << 30, max_kv=20000,
+           **kw):
+    from test_serving_host import cache
+
+    return lib.kv_cache_attention_masked(
+        ctypes.byref(kw.get("c") or cache()), FAKE, 512, 4, FAKE, FAKE, FAKE, 400, 400, kw.get("seqs", 2), 8,
+        max_q, max_kv, 0.1, window, sinks, masks, words, FAKE, 512, None, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(sinks=-1), dict(sinks=1 << 31), dict(words=0), dict(words=-1), dict(words=1 << 31),
+    dict(max_q=65), dict(words=2, max_q=129), dict(masks=FAKE + 4), dict(window=-1), dict(ws=None),
+    dict(ws=FAKE + 8), dict(ws_bytes=16)])
+def test_masked_refusals(lib, kw):
+    assert masked(lib, **kw) == INVALID
+    assert lib.bsq_serving_last_error()
+
+
+def test_masked_nothing_to_do(lib):
+    assert masked(lib, seqs=0) == OK and masked(lib, max_q=0, words=0) == OK
+
+
+def test_masked_workspace(lib):
+    """Without sinks that of kv_cache_attention; sinks lengthen a window's pages."""
+    w, m = lib.kv_cache_attention_workspace, lib.kv_cache_attention_masked_workspace
+    for a in ((2, 128, 4, 2, 8, 1, 100000), (8, 64, 32, 3, 60, 20, 5000), (1, 256, 8, 9, 9, 1, 70000)):
+        for window in (0, 100, 4000):
+            assert m(*a, window, 0) == w(*a, window)
+    assert m(2, 128, 4, 2, 8, 1, 100000, 300, 100) == 0
+    assert m(2, 128, 4, 2, 8, 1, 100000, 300, 50000) > 0
+    assert m(2, 128, 4, 2, 8, 1, 100000, 300, -1) == -1 and lib.bsq_serving_last_error()
+
+
+def test_reference_masks():
+    """The reference's masks by hand: 5 rows after 4 tokens."""
+    def see(*a):
+        return np.nonzero(R.seen_tokens(*a))[0].tolist()
+    assert see(9, 5, 2, 0, 0, None) == [0, 1, 2, 3, 4, 5, 6]
+    assert see(9, 5, 2, 3, 0, None) == [4, 5, 6] and see(9, 5, 2, 3, 2, None) == [0, 1, 4, 5, 6]
+    assert see(9, 5, 4, 0, 0, {0, 3}) == [0, 1, 2, 3, 4, 7]
+    assert see(9, 5, 4, 3, 0, {0, 3}) == [3, 4, 7] and see(9, 5, 4, 3, 1, {0, 3}) == [0, 3, 4, 7]
+    assert see(9, 5, 4, 1, 0, {0, 3}) == [4, 7] and see(9, 5, 4, 0, 0, set()) == [0, 1, 2, 3]
+    assert see(2, 5, 4, 0, 0, {0, 3, 4}) == [0, 1] and see(2, 5, 1, 0, 0, None) == []
+    assert R.words([{0, 64, 63}, set()], 2).tolist() == [[1 - (1 << 63), 1], [0, 0]]
+
+
+def test_reference_attention_is_the_causal_one():
+    import serving_ref as S
+
+    rng = np.random.default_rng(1)
+    c = S.Cache(3, 1, 64)
+    k = S.bf16(rng.standard_normal((130, 1, 64)))
+    S.append(c, k, k, [0, 130], [130], [[2, 0, 1]])
+    q = S.bf16(rng.standard_normal((4, 2, 64)))
+    chain = [set(range(i + 1)) for i in range(4)]
+    for window in (0, 60):
+        want = S.attention(c, q, [0, 4], [130], [[2, 0, 1]], 0.125, window)
+        for masks in (None, chain):
+            got = R.attention(c, q, [0, 4], [130], [[2, 0, 1]], 0.125, window, 0, masks)
+            assert all(np.allclose(a, b, rtol=1e-12, atol=0) for a, b in zip(got, want))
+    tree = R.attention(c, q, [0, 4], [130], [[2, 0, 1]], 0.125, 0, 0, [{0}, {1}, {0, 2}, {1, 3}])
+    causal = S.attention(c, q, [0, 4], [130], [[2, 0, 1]], 0.125)
+    off = np.abs(tree[0] - causal[0]) > causal[2]
+    assert off[1:].any((1, 2)).all() and not off[0].any()    # the bounds tell one token less
