@@ -474,8 +474,9 @@ def _ceiling():
 # The serving operators (8-bit KV cache, its pages, mixture of experts for a few tokens) have
 # libraries of their own, loaded when one of these names is first used.
 _SERVING = ("KV_PAGE", "KvCache", "kv_cache", "kv_cache_append", "kv_cache_attention",
-            "kv_cache_attention_masked", "kv_pages_compact", "kv_pages_copy", "kv_pages_fork", "kv_pages_free",
-            "kv_pages_reserve", "moe_few_tokens", "qk_norm_rope", "serving_lib")
+            "kv_cache_attention_masked", "kv_pages_compact", "kv_pages_copy", "kv_pages_fork",
+            "kv_pages_free", "kv_pages_reserve", "moe_few_tokens", "moe_group_rows", "moe_route",
+            "qk_norm_rope", "serving_lib")
 
 
 def __getattr__(name):

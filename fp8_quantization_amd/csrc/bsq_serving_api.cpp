@@ -180,6 +180,23 @@ int check_pages(const bsq_kv_cache* cache, const void* a, const void* b, int64_t
     return BSQ_OK;
 }
 
+// The entries of a moe_group_rows call, and how they are cut.
+int check_group(int64_t num_tokens, int64_t topk, int64_t num_experts, bsq::GroupArgs* a) {
+    if (num_tokens < 0 || num_tokens > kMaxInt || topk < 1 || topk > kMaxInt ||
+        num_tokens * topk > kMaxInt)
+        return fail(BSQ_ERR_INVALID_ARG,
+                    "num_tokens=%lld must be >= 0, topk=%lld >= 1, their product at most 2^31 - 1",
+                    (long long)num_tokens, (long long)topk);
+    if (num_experts < 1 || num_experts > bsq::kMoeMaxExperts)
+        return fail(BSQ_ERR_INVALID_ARG, "num_experts=%lld must be in 1 .. %d", (long long)num_experts,
+                    bsq::kMoeMaxExperts);
+    a->entries = num_tokens * topk;
+    a->topk = (int32_t)topk;
+    a->experts = (int32_t)num_experts;
+    bsq::plan_group(*a);
+    return BSQ_OK;
+}
+
 int check_slots(int64_t num_pages, const void* refcounts, const void* slots, int64_t n) {
     if (num_pages < 0 || num_pages > kMaxInt || n < 0 || n > kMaxInt)
         return fail(BSQ_ERR_INVALID_ARG, "num_pages=%lld and n=%lld must be in 0 .. 2^31 - 1",
@@ -576,6 +593,101 @@ int qk_norm_rope(int dtype, const void* q, int64_t ldq, int64_t num_q_heads, con
         return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
     return launched(bsq::launch_rope(a, dtype == BSQ_FP32, interleaved != 0,
                                      static_cast<hipStream_t>(stream)));
+}
+
+int moe_route(int dtype, const void* logits, int64_t ldl, int64_t num_tokens, int64_t num_experts,
+              int64_t topk, int score, const float* bias, int64_t num_groups, int64_t topk_groups,
+              int group_top, int renormalize, float factor, int32_t* topk_ids, float* topk_weights,
+              void* stream) {
+    const int st = check_dtype(dtype);
+    if (st != BSQ_OK) return st;
+    if (score != BSQ_SCORE_SOFTMAX && score != BSQ_SCORE_SIGMOID)
+        return fail(BSQ_ERR_UNSUPPORTED, "score %d is not provided (softmax or sigmoid)", score);
+    if (num_tokens < 0 || num_tokens > kMaxInt)
+        return fail(BSQ_ERR_INVALID_ARG, "num_tokens=%lld must be in 0 .. 2^31 - 1",
+                    (long long)num_tokens);
+    if (num_experts < 1 || num_experts > bsq::kMoeMaxExperts)
+        return fail(BSQ_ERR_INVALID_ARG, "num_experts=%lld must be in 1 .. %d", (long long)num_experts,
+                    bsq::kMoeMaxExperts);
+    if (num_groups < 1 || num_groups > 64 || num_experts % num_groups != 0 || topk_groups < 1 ||
+        topk_groups > num_groups || group_top < 1 || group_top > 2)
+        return fail(BSQ_ERR_INVALID_ARG,
+                    "num_groups=%lld must be in 1 .. 64 and divide num_experts=%lld, topk_groups=%lld "
+                    "be in 1 .. num_groups, group_top=%d 1 or 2", (long long)num_groups,
+                    (long long)num_experts, (long long)topk_groups, group_top);
+    if (topk < 1 || topk > bsq::kMoeMaxTopk || topk > num_experts / num_groups * topk_groups)
+        return fail(BSQ_ERR_INVALID_ARG, "topk=%lld must be in 1 .. %d and at most the %lld experts kept",
+                    (long long)topk, bsq::kMoeMaxTopk,
+                    (long long)(num_experts / num_groups * topk_groups));
+    if (!std::isfinite(factor)) return fail(BSQ_ERR_INVALID_ARG, "factor must be finite");
+    if (num_tokens == 0) return ok();
+    if (!logits || !topk_ids || !topk_weights)
+        return fail(BSQ_ERR_INVALID_ARG, "null pointer (logits=%p topk_ids=%p topk_weights=%p)", logits,
+                    topk_ids, topk_weights);
+    if (!aligned(logits, dtype == BSQ_FP32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_ids, 4) ||
+        !aligned(topk_weights, 4))
+        return fail(BSQ_ERR_INVALID_ARG, "every array must be aligned to its elements' size");
+    if (ldl < num_experts)
+        return fail(BSQ_ERR_INVALID_ARG, "the row stride %lld of logits must be >= %lld", (long long)ldl,
+                    (long long)num_experts);
+    if (!fits((double)num_tokens, 64)) return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
+    bsq::RouteArgs a{};
+    a.logits = logits;
+    a.ldl = ldl;
+    a.bias = bias;
+    a.ids = topk_ids;
+    a.weights = topk_weights;
+    a.tokens = num_tokens;
+    a.factor = factor;
+    a.experts = (int32_t)num_experts;
+    a.topk = (int32_t)topk;
+    a.groups = (int32_t)num_groups;
+    a.keep = (int32_t)topk_groups;
+    a.group_top = group_top;
+    a.sigmoid = score == BSQ_SCORE_SIGMOID;
+    a.renormalize = renormalize;
+    bsq::plan_route(a);
+    return launched(bsq::launch_route(a, dtype == BSQ_FP32, static_cast<hipStream_t>(stream)));
+}
+
+int64_t moe_group_rows_workspace(int64_t num_tokens, int64_t topk, int64_t num_experts) {
+    bsq::GroupArgs a{};
+    if (check_group(num_tokens, topk, num_experts, &a) != BSQ_OK) return -1;
+    ok();
+    return a.tiles == 1 ? 0 : (int64_t)a.tiles * num_experts * (int64_t)sizeof(int32_t);
+}
+
+int moe_group_rows(const int32_t* topk_ids, int64_t num_tokens, int64_t topk, int64_t num_experts,
+                   int64_t pad, uint32_t* row_offsets, uint32_t* scales_offsets,
+                   int32_t* row_indices, int32_t* entry_rows, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+    bsq::GroupArgs a{};
+    const int st = check_group(num_tokens, topk, num_experts, &a);
+    if (st != BSQ_OK) return st;
+    if (pad < 1 || pad > 65536)
+        return fail(BSQ_ERR_INVALID_ARG, "pad=%lld must be in 1 .. 65536", (long long)pad);
+    if (a.entries + num_experts * (pad - 1) > 0xFFFFFFFFLL)
+        return fail(BSQ_ERR_INVALID_ARG, "more than 2^32 - 1 scale rows");
+    if (!row_offsets || !scales_offsets || (a.entries > 0 && (!topk_ids || !row_indices)))
+        return fail(BSQ_ERR_INVALID_ARG,
+                    "null pointer (topk_ids=%p row_offsets=%p scales_offsets=%p row_indices=%p)",
+                    topk_ids, row_offsets, scales_offsets, row_indices);
+    if (!aligned(topk_ids, 4) || !aligned(row_offsets, 4) || !aligned(scales_offsets, 4) ||
+        !aligned(row_indices, 4) || !aligned(entry_rows, 4))
+        return fail(BSQ_ERR_INVALID_ARG, "every array must be aligned to its elements' size");
+    const int64_t need = moe_group_rows_workspace(num_tokens, topk, num_experts);
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+        return fail(BSQ_ERR_INVALID_ARG,
+                    "workspace (%p, %lld bytes) must be 16-byte aligned and hold %lld bytes",
+                    workspace, (long long)workspace_bytes, (long long)need);
+    a.ids = topk_ids;
+    a.row_offsets = row_offsets;
+    a.scales_offsets = scales_offsets;
+    a.row_indices = row_indices;
+    a.entry_rows = entry_rows;
+    a.counts = static_cast<int32_t*>(workspace);
+    a.pad = (uint32_t)pad;
+    return launched(bsq::launch_group(a, static_cast<hipStream_t>(stream)));
 }
 
 const char* bsq_serving_last_error(void) { return g_last_error; }

@@ -1,6 +1,6 @@
 // bsq_serving_internal.h -- launch interface between the host layer of
 // libbsq_serving (bsq_serving_api.cpp) and its gfx950 kernels (bsq_kv.hip,
-// bsq_pages.hip, bsq_moe.hip, bsq_rope.hip).  Not installed.
+// bsq_pages.hip, bsq_moe.hip, bsq_rope.hip, bsq_route.hip).  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -160,5 +160,39 @@ struct RopeArgs {
 };
 void plan_rope(RopeArgs& a);         // seg_steps and what follows, from the sizes
 hipError_t launch_rope(const RopeArgs& a, bool f32, bool pairs, hipStream_t stream);
+
+struct RouteArgs {
+    const void* logits;
+    int64_t ldl;                     // elements
+    const float* bias;               // nullable
+    int32_t* ids;
+    float* weights;
+    int64_t tokens;
+    float factor;
+    int32_t experts, topk, groups, keep, group_top;
+    int32_t sigmoid, renormalize;
+    int32_t group_size;              // experts of a group,
+    uint32_t group_magic;            // e * group_magic >> 20 = e / group_size for every expert e,
+    int32_t group_lanes;             // lanes that look at a group: a power of two
+};
+void plan_route(RouteArgs& a);       // group_size and what follows
+hipError_t launch_route(const RouteArgs& a, bool f32, hipStream_t stream);
+
+struct GroupArgs {
+    const int32_t* ids;
+    int64_t entries;
+    uint32_t* row_offsets;
+    uint32_t* scales_offsets;
+    int32_t* row_indices;
+    int32_t* entry_rows;             // nullable
+    int32_t* counts;                 // [tiles][experts], workspace of more than one tile
+    int32_t topk, experts;
+    uint32_t pad;
+    int64_t tile;                    // entries of a workgroup
+    int32_t tiles, bits;             // bits of the numbers 0 .. experts
+    int32_t count_lanes;             // threads that read consecutive counts of a tile
+};
+void plan_group(GroupArgs& a);       // tile and what follows
+hipError_t launch_group(const GroupArgs& a, hipStream_t stream);
 
 }  // namespace bsq

@@ -623,6 +623,87 @@ PyObject* rope(Args& a) {
     return r;
 }
 
+// A 2-D tensor of rows without gaps of BF16 or FP32 elements.
+const at::Tensor& logits_of(const at::Tensor* t) {
+    dtype_of(*t, "logits");
+    if (t->dim() != 2 || !dense_rows(*t))
+        refuse(0, "logits must be a 2-D GPU tensor, contiguous within a row");
+    return *t;
+}
+
+// logits, topk, score, bias, num_groups, topk_groups, group_top, renormalize, factor, topk_ids,
+// topk_weights, stream -> (ids, weights)
+PyObject* route(Args& a) {
+    const at::Tensor& logits = logits_of(a.tensor("logits"));
+    const int64_t k = a.integer("topk"), score = a.integer("score");
+    const at::Tensor* bias = a.tensor("bias", true);
+    const int64_t groups = a.integer("num_groups"), keep = a.integer("topk_groups");
+    const int64_t top = a.integer("group_top"), renormalize = a.integer("renormalize");
+    const double factor = a.number("factor");
+    const at::Tensor* ids = a.tensor("topk_ids", true);
+    const at::Tensor* weights = a.tensor("topk_weights", true);
+    const CallStream stream(a);
+    const int64_t T = logits.size(0), E = logits.size(1);
+    if (k < 1) refuse(BSQ_ERR_INVALID_ARG, "topk=%lld must be at least 1", (long long)k);
+    if (top < 1 || top > 2) refuse(BSQ_ERR_INVALID_ARG, "group_top=%lld must be 1 or 2", (long long)top);
+    if (bias) vec(bias, "bias", at::kFloat, E, true);
+    at::Tensor new_ids, new_weights;
+    if (!ids) {
+        new_ids = empty({T, k}, at::kInt, *a.device);
+        ids = &new_ids;
+    }
+    if (!weights) {
+        new_weights = empty({T, k}, at::kFloat, *a.device);
+        weights = &new_weights;
+    }
+    matrix(ids, "topk_ids", at::kInt, T, k);
+    matrix(weights, "topk_weights", at::kFloat, T, k);
+    check(moe_route(dtype_of(logits, "logits"), logits.data_ptr(), row_stride(logits), T, E, k,
+                    (int)score, bias ? bias->data_ptr<float>() : nullptr, groups, keep, (int)top,
+                    renormalize != 0, (float)factor, ids->data_ptr<int32_t>(),
+                    weights->data_ptr<float>(), stream.raw));
+    PyObject* o[2] = {stream.give(*ids, new_ids), stream.give(*weights, new_weights)};
+    PyObject* r = o[0] && o[1] ? PyTuple_Pack(2, o[0], o[1]) : nullptr;
+    for (PyObject* p : o) Py_XDECREF(p);
+    return r;
+}
+
+// topk_ids, num_experts, pad, row_offsets, scales_offsets, row_indices, entry_rows, workspace,
+// stream -> (row_offsets, scales_offsets, row_indices, entry_rows)
+PyObject* group_rows(Args& a) {
+    const at::Tensor& ids = *a.tensor("topk_ids");
+    const int64_t E = a.integer("num_experts"), pad = a.integer("pad");
+    const at::Tensor* out[4];
+    static const char* const names[4] = {"row_offsets", "scales_offsets", "row_indices", "entry_rows"};
+    for (int i = 0; i < 4; ++i) out[i] = a.tensor(names[i], true);
+    const at::Tensor* given = a.tensor("workspace", true);
+    const CallStream stream(a);
+    if (ids.scalar_type() != at::kInt || ids.dim() != 2 || !ids.is_contiguous())
+        refuse(0, "topk_ids must be a contiguous 2-D GPU tensor of dtype int32");
+    const int64_t T = ids.size(0), k = ids.size(1), n = T * k;
+    const int64_t need = size_of(moe_group_rows_workspace(T, k, E));
+    at::Tensor own[4];
+    for (int i = 0; i < 4; ++i) {
+        if (!out[i]) {
+            own[i] = i < 2 ? empty({E + 1}, at::kInt, *a.device)
+                           : i == 2 ? empty({n}, at::kInt, *a.device) : empty({T, k}, at::kInt, *a.device);
+            out[i] = &own[i];
+        }
+        if (i < 2) vec(out[i], names[i], at::kUInt32, E + 1, true);
+        else if (i == 2) vec(out[i], names[i], at::kInt, n, false);
+        else matrix(out[i], names[i], at::kInt, T, k);
+    }
+    const Workspace ws(a, need ? given : nullptr, need);
+    check(moe_group_rows(ids.data_ptr<int32_t>(), T, k, E, pad, static_cast<uint32_t*>(out[0]->data_ptr()),
+                         static_cast<uint32_t*>(out[1]->data_ptr()), out[2]->data_ptr<int32_t>(),
+                         out[3]->data_ptr<int32_t>(), ws.p, ws.bytes, stream.raw));
+    PyObject* o[4];
+    for (int i = 0; i < 4; ++i) o[i] = stream.give(*out[i], own[i]);
+    PyObject* r = o[0] && o[1] && o[2] && o[3] ? PyTuple_Pack(4, o[0], o[1], o[2], o[3]) : nullptr;
+    for (PyObject* p : o) Py_XDECREF(p);
+    return r;
+}
+
 #define ENTRY(name, fn) {name, (PyCFunction)(void (*)(void))entry<fn>, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY("init", init),
                            ENTRY("append", append),
@@ -634,6 +715,8 @@ PyMethodDef g_methods[] = {ENTRY("init", init),
                            ENTRY("pages_compact", pages_compact),
                            ENTRY("moe", moe),
                            ENTRY("rope", rope),
+                           ENTRY("route", route),
+                           ENTRY("group_rows", group_rows),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -53,6 +53,9 @@ for _name, _res, *_args in (
         ("kv_cache_attention_masked_workspace", _i64, *[_i64] * 9),
         ("qk_norm_rope", _i32, _i32, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _p, _p,
          _f32, _p, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _i64, _p),
+        ("moe_route", _i32, _i32, _p, *[_i64] * 4, _i32, _p, _i64, _i64, _i32, _i32, _f32, _p, _p, _p),
+        ("moe_group_rows", _i32, _p, *[_i64] * 4, _p, _p, _p, _p, _p, _i64, _p),
+        ("moe_group_rows_workspace", _i64, *[_i64] * 3),
         ("bsq_serving_last_error", ctypes.c_char_p)):
     getattr(_lib, _name).restype, getattr(_lib, _name).argtypes = _res, _args
 
@@ -207,3 +210,38 @@ def kv_cache_attention_masked(q: torch.Tensor, cache: KvCache, row_offsets: torc
                            q.shape[-1] ** -0.5 if scale is None else scale, window, out, lse,
                            return_lse, workspace, sinks, masks, stream)
     return r if return_lse else r[0]
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", bias=None,
+              num_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+              renormalize: bool = True, factor: float = 1.0, topk_ids=None, topk_weights=None,
+              stream=None):
+    """Experts of each token from a router's ``logits`` (BF16 or FP32 [tokens,
+    experts]): scores by ``score`` ("softmax" or "sigmoid"), the ``topk``
+    largest of score + ``bias`` (fp32 [experts]) among the ``topk_groups`` of
+    ``num_groups`` groups whose ``group_top`` (1 or 2) largest have the largest
+    sum.  Weights are ``factor`` times the scores, divided by the sum of the
+    chosen ones with ``renormalize``.  The choice is that of 64-bit arithmetic,
+    ties to the lower number.  Returns (topk_ids int32, topk_weights fp32)
+    [tokens, topk], as ``moe_few_tokens`` takes them."""
+    if score not in SCORES:
+        raise BsqError(2, f"score={score!r} is not provided (softmax or sigmoid)")
+    return _serving.route(logits, topk, SCORES[score], bias, num_groups, topk_groups, group_top,
+                          renormalize, factor, topk_ids, topk_weights, stream)
+
+
+def moe_group_rows(topk_ids: torch.Tensor, num_experts: int, pad: int = 128, row_offsets=None,
+                   scales_offsets=None, row_indices=None, entry_rows=None, workspace=None,
+                   stream=None):
+    """The routed rows of each expert for the grouped quantizer and GEMM, from
+    ``topk_ids`` (int32 [tokens, topk]; numbers outside the experts have no
+    row), an expert's entries in their order.  Returns int32 (row_offsets
+    [experts + 1], scales_offsets [experts + 1], a group's scale rows being
+    its rows rounded up to a multiple of ``pad``, row_indices [tokens * topk],
+    the token of each routed row or -1 past the last, entry_rows [tokens, topk],
+    the routed row of each entry or -1)."""
+    return _serving.group_rows(topk_ids, num_experts, pad, row_offsets, scales_offsets, row_indices,
+                               entry_rows, workspace, stream)

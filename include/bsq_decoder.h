@@ -96,6 +96,69 @@ int64_t kv_cache_attention_masked_workspace(int64_t num_heads, int64_t head_dim,
                                             int64_t num_rows, int64_t max_q, int64_t max_kv,
                                             int64_t window, int64_t sinks);
 
+/*
+ * Experts of each token from a router's logits z, and their weights.
+ *
+ *   s = softmax(z) (BSQ_SCORE_SOFTMAX) or 1 / (1 + exp(-z)) (BSQ_SCORE_SIGMOID)
+ *   c = s + bias   (the bias takes part in the choice alone)
+ *   of num_groups groups of num_experts / num_groups consecutive experts, the
+ *     topk_groups with the largest sum of their group_top (1 or 2) largest c
+ *     are kept;
+ *   the topk largest c of the kept groups' experts are chosen, the largest
+ *     first; equal groups and experts go by their number, the lower first;
+ *   weight = factor * s, with renormalize != 0 divided by the sum of the
+ *     chosen s.
+ *
+ * The choice is that of c in 64-bit arithmetic: values that 32 bits cannot
+ * tell apart are computed again.  (Without a bias c goes by z, and z is
+ * compared instead, but for sums of two.)  A logit of -inf or NaN, or a bias
+ * of -inf or NaN, makes c -inf: chosen only where nothing else is left, with
+ * weight 0.  Under softmax a logit of +inf takes the whole score, shared with
+ * its equals.  Where the chosen s are all 0, so are the weights.
+ *
+ *   dtype         of the logits [num_tokens][num_experts], ldl elements from
+ *                 a row to the next, aligned to their size.
+ *   num_experts   1 .. 1024;  topk 1 .. 16 and at most the experts kept.
+ *   bias          fp32 [num_experts], or NULL.
+ *   num_groups    1 .. 64, a divisor of num_experts;  topk_groups 1 ..
+ *                 num_groups.  group_top above a group's size counts as it.
+ *   factor        finite.
+ *   topk_ids, topk_weights   int32 / fp32 [num_tokens][topk], as
+ *                 moe_few_tokens takes them.
+ */
+enum bsq_score { BSQ_SCORE_SOFTMAX = 0, BSQ_SCORE_SIGMOID = 1 };
+int moe_route(int dtype, const void* logits, int64_t ldl, int64_t num_tokens, int64_t num_experts,
+              int64_t topk, int score, const float* bias, int64_t num_groups, int64_t topk_groups,
+              int group_top, int renormalize, float factor, int32_t* topk_ids, float* topk_weights,
+              void* stream);
+
+/*
+ * The routed rows of each expert, as the grouped calls of bsq.h take them:
+ * entry (token t, place j) of topk_ids goes to the group of its expert, the
+ * entries of an expert in their order (t, then j).
+ *
+ *   topk_ids        int32 [num_tokens][topk]; an entry outside num_experts has
+ *                   no row.
+ *   pad             1 .. 65536: scale rows of a group are its rows rounded up
+ *                   to a multiple of pad (the MFMA scale layout takes 16).
+ *   row_offsets, scales_offsets   uint32 [num_experts + 1].
+ *   row_indices     int32 [num_tokens * topk]: the token of each routed row,
+ *                   -1 past the last.
+ *   entry_rows      int32 [num_tokens][topk]: the routed row of each entry, -1
+ *                   for none; or NULL.
+ *   num_experts     1 .. 1024;  num_tokens * topk at most 2^31 - 1, and with
+ *                   num_experts * (pad - 1) at most 2^32 - 1.
+ *   workspace       16-byte aligned, moe_group_rows_workspace(...) bytes (0: may
+ *                   be NULL).
+ * expert_ids of the grouped calls are the numbers 0 .. num_experts - 1.
+ * No tokens: the offsets are written, all 0.
+ */
+int moe_group_rows(const int32_t* topk_ids, int64_t num_tokens, int64_t topk, int64_t num_experts,
+                   int64_t pad, uint32_t* row_offsets, uint32_t* scales_offsets,
+                   int32_t* row_indices, int32_t* entry_rows, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+int64_t moe_group_rows_workspace(int64_t num_tokens, int64_t topk, int64_t num_experts);
+
 #ifdef __cplusplus
 }
 #endif

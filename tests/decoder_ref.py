@@ -114,3 +114,81 @@ def random_tree(rng, n, most_back=6):
         parent = i - int(rng.integers(1, most_back + 1))
         masks.append((masks[parent] if parent >= 0 else set()) | {i})
     return masks
+
+
+# ------------------------------------------------------------------ routing
+
+
+def route(logits, topk, score, bias=None, groups=1, keep=1, top=1, renormalize=True, factor=1.0):
+    """(ids, weights, bound of the weights) of moe_route on float64 logits [tokens, experts].
+
+    An exponential of v (the hardware's base-2 one, its argument rounded) is off by (|v| + 2) 2 U,
+    relative; sums add their terms' errors and U for each of up to 22 additions; a quotient, a
+    product and 1 + t follow, 6 U; what falls below the smallest normal number may be lost."""
+    T, E = logits.shape
+    ids, weights, bound = np.zeros((T, topk), int), np.zeros((T, topk)), np.zeros((T, topk))
+    b = np.zeros(E) if bias is None else np.where(np.isnan(bias), -np.inf, bias)
+    size = E // groups
+    for t in range(T):
+        z = np.where(np.isnan(logits[t]), -np.inf, logits[t])
+        with np.errstate(over="ignore", invalid="ignore"):
+            if score == "sigmoid":
+                s = 1 / (1 + np.exp(-z))
+            else:
+                s = np.where(z == z.max(), 1.0, np.exp(z - z.max())) * (z > -np.inf)
+                s = s / s.sum() if s.sum() else s
+        c = np.where((z == -np.inf) | (b == -np.inf), -np.inf, s + b)
+        # without a bias c goes by z, of which the scores may lose the difference
+        order = z if bias is None else c
+        if groups > 1:
+            def of(g):
+                best = sorted(c[g * size:(g + 1) * size])[::-1][:min(top, size)]
+                if bias is None and len(best) == 1:
+                    return order[g * size:(g + 1) * size].max()
+                return -np.inf if -np.inf in best else sum(best)
+            kept = sorted(range(groups), key=lambda g: (-of(g), g))[:keep]
+            open_ = [e for e in range(E) if e // size in kept]
+        else:
+            open_ = list(range(E))
+        ids[t] = sorted(open_, key=lambda e: (-order[e], e))[:topk]
+        y = np.where(c[ids[t]] == -np.inf, -np.inf, z[ids[t]])
+        if score == "sigmoid":
+            m = min(y.max(), 0.0) if renormalize and y.max() > -np.inf else 0.0
+            v = np.where(y > 0, -y, y - m)
+            with np.errstate(over="ignore", invalid="ignore"):
+                w = np.where(y == -np.inf, 0.0, np.exp(np.minimum(y, 0) - m) / (1 + np.exp(-np.abs(y))))
+            v, den, far = np.where(y == -np.inf, 0, np.abs(np.minimum(y, 0) - m) + np.minimum(np.abs(y), 90)), 1.0, 0.0
+            if renormalize:
+                den = w.sum()
+                far = (w * (v + 2)).sum() / den if den else 0.0
+        else:
+            pool = y if renormalize else z
+            m = pool.max()
+            with np.errstate(invalid="ignore"):
+                w = np.where(y == m, 1.0, np.exp(y - m)) * (y > -np.inf)
+                all_ = np.where(pool == m, 1.0, np.exp(pool - m)) * (pool > -np.inf)
+                v = np.where(w > 0, np.where(y == m, 0.0, m - y), 0.0)
+                va = np.where(all_ > 0, np.where(pool == m, 0.0, m - pool), 0.0)
+            den = all_.sum()
+            far = (all_ * (va + 2)).sum() / den if den else 0.0
+        weights[t] = factor * w / den if den else 0.0
+        bound[t] = np.abs(weights[t]) * ((v + 2 + far) * 2 + 28) * U + abs(factor) * 2.0 ** -125
+    return ids, weights, bound
+
+
+def group_rows(ids, experts, pad):
+    """moe_group_rows with loops."""
+    T, k = ids.shape
+    groups = [[] for _ in range(experts)]
+    for t in range(T):
+        for j in range(k):
+            if 0 <= ids[t, j] < experts:
+                groups[ids[t, j]].append((t, j))
+    rows, scales = [0], [0]
+    index, entry = np.full(T * k, -1), np.full((T, k), -1)
+    for g in groups:
+        for i, (t, j) in enumerate(g):
+            index[rows[-1] + i], entry[t, j] = t, rows[-1] + i
+        rows.append(rows[-1] + len(g))
+        scales.append(scales[-1] + (len(g) + pad - 1) // pad * pad)
+    return np.array(rows), np.array(scales), index, entry

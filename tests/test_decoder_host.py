@@ -139,3 +139,72 @@ def test_reference_attention_is_the_causal_one():
     causal = S.attention(c, q, [0, 4], [130], [[2, 0, 1]], 0.125)
     off = np.abs(tree[0] - causal[0]) > causal[2]
     assert off[1:].any((1, 2)).all() and not off[0].any()    # the bounds tell one token less
+
+
+# ------------------------------------------------------------------ routing
+
+
+def route(lib, dtype=1, z=FAKE, ldl=64, T=5, E=64, k=6, score=0, bias=FAKE, groups=8, keep=3, top=2,
+          renorm=1, factor=1.0, ids=FAKE, w=FAKE):
+    return lib.moe_route(dtype, z, ldl, T, E, k, score, bias, groups, keep, top, renorm, factor, ids, w, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=2), UNSUPPORTED), (dict(score=2), UNSUPPORTED), (dict(score=-1), UNSUPPORTED),
+    (dict(T=-1), INVALID), (dict(T=1 << 31), INVALID), (dict(E=0), INVALID),
+    (dict(E=1025, groups=1, ldl=2000), INVALID), (dict(groups=0), INVALID), (dict(groups=7), INVALID),
+    (dict(E=65, ldl=65, groups=65), INVALID), (dict(keep=0), INVALID), (dict(keep=9), INVALID),
+    (dict(top=0), INVALID), (dict(top=3), INVALID), (dict(k=0), INVALID), (dict(k=17), INVALID),
+    (dict(k=9, keep=1), INVALID), (dict(factor=float("inf")), INVALID), (dict(z=None), INVALID),
+    (dict(ids=None), INVALID), (dict(w=None), INVALID), (dict(ldl=63), INVALID),
+    (dict(z=FAKE + 2), INVALID), (dict(dtype=0, z=FAKE + 1), INVALID), (dict(bias=FAKE + 2), INVALID),
+    (dict(T=1 << 27), INVALID)])
+def test_route_refusals(lib, kw, status):
+    assert route(lib, **kw) == status
+    assert lib.bsq_serving_last_error()
+
+
+def test_route_nothing_to_do(lib):
+    assert route(lib, T=0, z=None, ids=None, w=None) == OK
+
+
+def group(lib, ids=FAKE, T=3000, k=8, E=64, pad=128, ro=FAKE, so=FAKE, ri=FAKE, er=FAKE, ws=FAKE, n=1 << 20):
+    return lib.moe_group_rows(ids, T, k, E, pad, ro, so, ri, er, ws, n, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(k=0), dict(T=1 << 28, k=8), dict(T=1 << 40, k=1 << 40), dict(E=0), dict(E=1025),
+    dict(pad=0), dict(pad=65537), dict(ids=None), dict(ro=None), dict(so=None), dict(ri=None),
+    dict(ws=None), dict(ws=FAKE + 8), dict(n=100), dict(ids=FAKE + 2), dict(er=FAKE + 1)])
+def test_group_refusals(lib, kw):
+    assert group(lib, **kw) == INVALID
+    assert lib.bsq_serving_last_error()
+
+
+def test_group_workspace(lib):
+    w = lib.moe_group_rows_workspace
+    assert w(0, 1, 8) == 0 and w(64, 8, 256) == 0
+    assert w(16384, 8, 256) > 0 and w(16384, 8, 256) % (256 * 4) == 0
+    assert w((1 << 31) - 1, 1, 1024) > 0
+    assert w(-1, 1, 8) == -1 and w(1, 0, 8) == -1 and w(1, 1, 0) == -1 and lib.bsq_serving_last_error()
+
+
+def test_reference_route_by_hand():
+    z = np.log([[1.0, 2, 3, 4, 5, 6, 7, 8]])
+    ids, w, _ = R.route(z, 2, "softmax", groups=4, keep=2, top=2, renormalize=False)
+    assert ids.tolist() == [[7, 6]] and np.allclose(w, [[8 / 36, 7 / 36]])
+    bias = np.array([0, 0, 1.0, 0, 0, 0, 0, 0])
+    ids, w, _ = R.route(z, 2, "softmax", bias=bias, groups=4, keep=2, factor=2.0)
+    assert ids.tolist() == [[2, 7]] and np.allclose(w, [[2 * 3 / 11, 2 * 8 / 11]])
+    ids, w, _ = R.route(z, 2, "sigmoid")
+    assert ids.tolist() == [[7, 6]] and np.allclose(w[0, 0] / w[0, 1], (8 / 9) / (7 / 8))
+    ids, w, _ = R.route(np.array([[-np.inf, np.nan, -np.inf, -900.0, -901.0]]), 3, "sigmoid")
+    assert ids.tolist() == [[3, 4, 0]] and np.allclose(w, [[1 / (1 + np.exp(-1)), 1 / (1 + np.e), 0]])
+    ids, w, _ = R.route(np.array([[1.0, np.inf, np.inf, 0.0]]), 3, "softmax")
+    assert ids.tolist() == [[1, 2, 0]] and w.tolist() == [[0.5, 0.5, 0.0]]
+
+
+def test_reference_rows_by_hand():
+    rows, scales, index, entry = R.group_rows(np.array([[2, 0], [0, 0], [-1, 3]]), 3, 4)
+    assert rows.tolist() == [0, 3, 3, 4] and scales.tolist() == [0, 4, 4, 8]
+    assert index.tolist() == [0, 1, 1, 0, -1, -1] and entry.tolist() == [[3, 0], [1, 2], [-1, -1]]

@@ -1,0 +1,264 @@
+"""Routing and the grouped rows on the GPU: chosen experts and rows exactly, weights within the
+reference's bounds; and the rows through the grouped quantizer and GEMM."""
+import numpy as np
+import pytest
+import torch
+
+import decoder_ref as R
+from test_gpu_serving_kv import bsq, i32  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def check(bsq, z, topk, dtype=torch.float32, bias=None, **kw):  # noqa: F811
+    x = torch.tensor(z, device="cuda").to(dtype)
+    b = None if bias is None else torch.tensor(bias, device="cuda").float()
+    names = dict(groups="num_groups", keep="topk_groups", top="group_top")
+    ids, w = bsq.moe_route(x, topk, bias=b, **{names.get(k, k): v for k, v in kw.items()})
+    torch.cuda.synchronize()
+    want, ww, bound = R.route(x.double().cpu().numpy(), topk, bias=None if b is None else b.double().cpu().numpy(),
+                              **{**dict(score="softmax"), **kw})
+    assert np.array_equal(ids.cpu().numpy(), want)
+    off = np.abs(w.double().cpu().numpy() - ww)
+    assert np.all(off <= bound), np.max(off / bound)
+    return ids, w
+
+
+SHAPES = [(1, 1, 1), (2, 8, 2), (5, 60, 6), (64, 128, 8), (7, 129, 16), (33, 256, 8), (3, 1000, 13), (4, 1024, 16)]
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sizes(bsq, T, E, k, score, bias, dtype):  # noqa: F811
+    rng = np.random.default_rng(T + E + k)
+    z, b = rng.standard_normal((T, E)) * 2, 0.1 * rng.standard_normal(E) if bias else None
+    for renorm, factor in ((True, 1.0), (False, 2.5)):
+        check(bsq, z, k, dtype, b, score=score, renormalize=renorm, factor=factor)
+
+
+@pytest.mark.parametrize("E,groups,keep", [(256, 8, 4), (64, 64, 20), (12, 3, 1), (160, 8, 3), (1024, 2, 1),
+                                           (1000, 40, 7), (6, 6, 6), (63, 9, 5)])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("score,bias", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_groups(bsq, E, groups, keep, top, score, bias):  # noqa: F811
+    rng = np.random.default_rng(E + groups)
+    z, b = rng.standard_normal((17, E)) * 2, 0.1 * rng.standard_normal(E) if bias else None
+    k = min(8, E // groups * keep)
+    check(bsq, z, k, bias=b, score=score, groups=groups, keep=keep, top=top, renormalize=top == 1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top", [(1, 1), (4, 1), (4, 2)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_equal_values_go_by_number(bsq, score, groups, top, bias):  # noqa: F811
+    rng = np.random.default_rng(9)
+    z = rng.integers(-1, 2, (40, 64)).astype(float)
+    z[0] = 0.0
+    z[1] = -0.0
+    z[1, ::2] = 0.0
+    b = rng.integers(0, 2, 64) * 0.5 if bias else None
+    check(bsq, z, 10, bias=b, score=score, groups=groups, keep=max(1, groups // 2), top=top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_values_that_32_bits_cannot_tell_apart(bsq, score):  # noqa: F811
+    """Biases that bring the scores of all experts to one value but for the rounding of the bias:
+    the order of 64 bits."""
+    rng = np.random.default_rng(3)
+    z = rng.standard_normal(96).astype(np.float32).astype(float)
+    s = 1 / (1 + np.exp(-z)) if score == "sigmoid" else np.exp(z) / np.exp(z).sum()
+    b = (1.5 - s).astype(np.float32).astype(float)
+    c = s + b
+    assert np.unique(c.astype(np.float32)).size < 12 and np.unique(c).size == 96
+    check(bsq, np.stack([z] * 3), 16, bias=b, score=score)
+    check(bsq, np.stack([z] * 3), 8, bias=b, score=score, groups=8, keep=3, top=2)
+    check(bsq, np.stack([z] * 3), 8, bias=b, score=score, groups=12, keep=5, top=1)
+    # pairs of experts whose sums alone decide between groups
+    z = np.repeat(rng.standard_normal((1, 32)), 4, 0).astype(np.float32).astype(float)
+    z = z.reshape(4, 8, 4).transpose(0, 2, 1).reshape(4, 32)
+    check(bsq, z, 4, score=score, groups=4, keep=2, top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("bias", [False, True])
+def test_special_logits(bsq, score, renorm, bias):  # noqa: F811
+    inf, nan = np.inf, np.nan
+    rng = np.random.default_rng(8)
+    z = rng.standard_normal((12, 16))
+    z[0] = -inf
+    z[1] = nan
+    z[2, :13] = -inf
+    z[3, ::2] = nan
+    z[4, 3] = z[4, 11] = inf
+    z[5] = 200 * z[5]
+    z[6] = -300 + z[6]
+    z[7] = 1e30 * np.sign(z[7])
+    z[8, :8] = -1e4
+    z[9] = [-3e38, 3e38] * 8
+    z[10] = 30 + 0.01 * z[10]
+    b = None
+    if bias:
+        b = 0.1 * rng.standard_normal(16)
+        b[2], b[3], b[5], b[9] = -inf, nan, inf, -5.0
+    for g in (dict(), dict(groups=4, keep=2), dict(groups=4, keep=2, top=2)):
+        if score == "sigmoid" and bias is False and g.get("top") == 2:
+            continue                 # sums of saturated scores: below, with a bias
+        check(bsq, z, 4, bias=b, score=score, renormalize=renorm, **g)
+
+
+def test_rows_of_a_larger_tensor(bsq):  # noqa: F811
+    """A row stride, an odd offset of BF16 elements, outputs of the caller's."""
+    rng = np.random.default_rng(2)
+    big = torch.tensor(rng.standard_normal((9, 77)), device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        x = big.to(dtype)[:, 3:64]
+        ids = torch.full((11, 5), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((11, 5), 7.0, device="cuda")
+        r = bsq.moe_route(x, 5, topk_ids=ids, topk_weights=w)
+        a = bsq.moe_route(x.contiguous(), 5)
+        torch.cuda.synchronize()
+        assert r[0] is ids and torch.equal(ids[:9], a[0]) and torch.equal(w[:9], a[1])
+        assert bool((ids[9:] == -7).all()) and bool((w[9:] == 7).all())
+
+
+def test_many_tokens(bsq):  # noqa: F811
+    rng = np.random.default_rng(1)
+    z = rng.standard_normal((1501, 64))
+    check(bsq, z, 6, bias=0.1 * rng.standard_normal(64), score="sigmoid", groups=8, keep=3, top=2, factor=-1.5)
+    ids, w = bsq.moe_route(torch.empty((0, 8), device="cuda"), 2)
+    assert ids.shape == (0, 2) and w.shape == (0, 2)
+
+
+def test_route_agrees_with_moe_few_tokens(bsq):  # noqa: F811
+    """Softmax routing chooses and weighs as moe_few_tokens does from the same logits."""
+    from test_gpu_serving_moe import Layer
+
+    rng = np.random.default_rng(4)
+    L = Layer(9, 12, 256, 128, "mxfp4")
+    x = torch.tensor(rng.standard_normal((9, 256)), device="cuda").to(torch.bfloat16)
+    z = torch.tensor(rng.standard_normal((9, 12)), device="cuda").float()
+    w = L.dev()
+    for renorm in (True, False):
+        y, ids, ws = bsq.moe_few_tokens(x, "mxfp4", *w, 12, 3, router_logits=z, renormalize=renorm)
+        i2, w2 = bsq.moe_route(z, 3, renormalize=renorm)
+        y2, _, _ = bsq.moe_few_tokens(x, "mxfp4", *w, 12, 3, topk_ids=i2, topk_weights=w2)
+        torch.cuda.synchronize()
+        assert torch.equal(ids, i2) and torch.allclose(ws, w2, rtol=1e-6, atol=0)
+        assert torch.allclose(y.float(), y2.float(), rtol=2 ** -7, atol=1e-3)
+
+
+# ------------------------------------------------------------------ grouped rows
+
+
+def check_rows(bsq, ids, E, pad, **kw):  # noqa: F811
+    got = bsq.moe_group_rows(i32(ids), E, pad=pad, **kw)
+    torch.cuda.synchronize()
+    want = R.group_rows(np.asarray(ids), E, pad)
+    for name, g, w in zip(("row_offsets", "scales_offsets", "row_indices", "entry_rows"), got, want):
+        assert np.array_equal(g.cpu().numpy(), w), name
+    return got
+
+
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 16), (3, 2), (63, 1), (64, 8), (65, 7), (512, 8), (513, 8), (700, 12),
+                                 (3000, 5)])
+@pytest.mark.parametrize("E,pad", [(1, 16), (2, 1), (63, 128), (64, 7), (256, 128), (1023, 16), (1024, 65536)])
+def test_group_rows(bsq, T, k, E, pad):  # noqa: F811
+    rng = np.random.default_rng(T + k + E)
+    check_rows(bsq, rng.integers(0, E, (T, k)), E, pad)
+    check_rows(bsq, rng.integers(-2, E + 2, (T, k)), E, pad)
+
+
+@pytest.mark.parametrize("T", [50, 2000])
+def test_group_rows_of_uneven_choices(bsq, T):  # noqa: F811
+    """Every entry one expert's; none anyone's; the same expert twice in a token; far numbers."""
+    check_rows(bsq, np.full((T, 4), 5), 9, 128)
+    check_rows(bsq, np.full((T, 4), -1), 9, 128)
+    check_rows(bsq, np.full((T, 4), 2 ** 31 - 1), 1024, 128)
+    check_rows(bsq, np.sort(np.random.default_rng(1).integers(0, 300, (T, 4)).reshape(-1)).reshape(T, 4), 300, 16)
+
+
+def test_group_rows_of_many_tiles(bsq):  # noqa: F811
+    rng = np.random.default_rng(5)
+    check_rows(bsq, (rng.random((60000, 5)) ** 3 * 200).astype(int), 200, 128)
+    r = bsq.moe_group_rows(torch.empty((0, 3), dtype=torch.int32, device="cuda"), 70)
+    torch.cuda.synchronize()
+    assert not r[0].any() and not r[1].any() and r[0].numel() == 71 and r[2].numel() == 0
+
+
+def test_group_rows_outputs_of_the_callers(bsq):  # noqa: F811
+    ids = np.random.default_rng(6).integers(0, 8, (900, 6))
+    want = check_rows(bsq, ids, 8, 16)
+    ro = torch.zeros(9, dtype=torch.uint32, device="cuda")
+    ri = torch.full((6000,), 9, dtype=torch.int32, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    got = bsq.moe_group_rows(i32(ids), 8, pad=16, row_offsets=ro, row_indices=ri, workspace=ws)
+    torch.cuda.synchronize()
+    assert got[0] is ro and torch.equal(ro.view(torch.int32), want[0])
+    assert torch.equal(ri[:5400], want[2]) and bool((ri[5400:] == 9).all())
+
+
+@pytest.mark.parametrize("T", [40, 900])
+def test_rows_through_the_grouped_calls(bsq, T):  # noqa: F811
+    """Route, group, quantize with the gather, multiply, and add up by entry_rows: equal to each
+    entry's own product."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    E, k, H, N = 10, 3, 256, 128
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn((E * N, H), generator=g, device="cuda").to(torch.bfloat16)
+    z = torch.randn((T, E), generator=g, device="cuda")
+    ids, weights = bsq.moe_route(z, k, score="sigmoid")
+    rows, scales, index, entry = bsq.moe_group_rows(ids, E, pad=128)
+    most = T * k + E * 127
+    most -= most % 128
+    experts = torch.arange(E, dtype=torch.int32, device="cuda")
+    wc, ws = bsq.quantize_block_scaled(w, "mxfp8", scale_layout=bsq.SCALES_MFMA16)
+    xc, xs = bsq.grouped_quantize_block_scaled(x, "mxfp8", rows, scales, experts, None, T * k, most,
+                                               row_indices=index, scale_layout=bsq.SCALES_MFMA16)
+    c = bsq.grouped_block_scaled_matmul_mfma(xc, xs, rows, scales, experts, T * k, most, wc, ws, E,
+                                             "mxfp8", H)
+    y = (c[entry.long()] * weights[..., None]).sum(1)
+    dq, ds = bsq.quantize_block_scaled(x, "mxfp8")
+    a = bsq.dequantize_block_scaled(dq, ds, "mxfp8", H).double()
+    dq, ds = bsq.quantize_block_scaled(w, "mxfp8")
+    b = bsq.dequantize_block_scaled(dq, ds, "mxfp8", H).double().view(E, N, H)
+    torch.cuda.synchronize()
+    want, size = torch.zeros((2, T, N), dtype=torch.float64, device="cuda")
+    for j in range(k):
+        for e in range(E):
+            t = (ids[:, j] == e).nonzero()[:, 0]
+            f = weights[t, j, None].double()
+            want[t] += f * (a[t] @ b[e].t().contiguous())
+            size[t] += f * (a[t].abs() @ b[e].abs().t().contiguous())
+    # two 128-element steps, each off by 2^-12 of its largest product at most, and fp32 sums
+    assert bool(((y - want).abs() <= size * 2.0 ** -11).all())
+
+
+def test_refusals_of_the_binding(bsq):  # noqa: F811
+    z, ids = torch.zeros((4, 16), device="cuda"), i32([[1, 2]] * 4)
+    b = torch.zeros(16, device="cuda")
+    for err, kw in [(TypeError, dict(logits=z.half())), (TypeError, dict(logits=z.cpu())),
+                    (TypeError, dict(logits=z[0])), (TypeError, dict(logits=z.t())),
+                    (TypeError, dict(bias=b.double())), (TypeError, dict(topk=1.5)),
+                    (TypeError, dict(topk_ids=ids.long())), (bsq.BsqError, dict(topk_ids=ids[:3])),
+                    (bsq.BsqError, dict(topk_weights=z[:, :3].contiguous())), (bsq.BsqError, dict(topk=0)),
+                    (bsq.BsqError, dict(topk=17)), (bsq.BsqError, dict(bias=b[:8])),
+                    (bsq.BsqError, dict(num_groups=3)), (bsq.BsqError, dict(num_groups=8, topk_groups=9)),
+                    (bsq.BsqError, dict(num_groups=16, topk_groups=1)), (bsq.BsqError, dict(group_top=3)),
+                    (bsq.BsqError, dict(factor=float("nan"))), (bsq.BsqError, dict(score="tanh"))]:
+        args = dict(logits=z, topk=2)
+        args.update(kw)
+        with pytest.raises(err):
+            bsq.moe_route(**args)
+    for err, kw in [(TypeError, dict(topk_ids=ids.long())), (TypeError, dict(topk_ids=ids[:, :1])),
+                    (TypeError, dict(topk_ids=ids[0])), (bsq.BsqError, dict(num_experts=0)),
+                    (bsq.BsqError, dict(num_experts=1025)), (bsq.BsqError, dict(pad=0)),
+                    (bsq.BsqError, dict(pad=65537)), (bsq.BsqError, dict(topk_ids=ids[:, :0])),
+                    (bsq.BsqError, dict(row_offsets=ids[:, 0].contiguous())),
+                    (bsq.BsqError, dict(row_indices=ids[:2].reshape(-1))), (TypeError, dict(entry_rows=z))]:
+        args = dict(topk_ids=ids, num_experts=4)
+        args.update(kw)
+        with pytest.raises(err):
+            bsq.moe_group_rows(**args)
