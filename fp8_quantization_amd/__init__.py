@@ -476,7 +476,7 @@ def _ceiling():
 _SERVING = ("KV_PAGE", "KvCache", "kv_cache", "kv_cache_append", "kv_cache_attention",
             "kv_cache_attention_masked", "kv_pages_compact", "kv_pages_copy", "kv_pages_fork",
             "kv_pages_free", "kv_pages_reserve", "moe_few_tokens", "moe_group_rows", "moe_route",
-            "qk_norm_rope", "serving_lib")
+            "qk_norm_rope", "serving_lib", "token_logprobs", "TokenLogprobs")
 
 
 def __getattr__(name):

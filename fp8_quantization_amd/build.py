@@ -25,7 +25,8 @@ CEILING_SOURCES = [os.path.join(CSRC, "bsq_ceiling.hip")]
 SERVING_LIB = os.path.join(HERE, "libbsq_serving.so")
 SERVING_SOURCES = [os.path.join(CSRC, f) for f in ("bsq_serving_api.cpp", "bsq_kv.hip",
                                                    "bsq_pages.hip", "bsq_moe.hip",
-                                                   "bsq_rope.hip", "bsq_route.hip")]
+                                                   "bsq_rope.hip", "bsq_route.hip",
+                                                   "bsq_logprobs.hip")]
 # their Python binding, a CPython extension over torch's C++ tensors
 SERVING_EXT = os.path.join(HERE, "_serving.so")
 

@@ -197,6 +197,28 @@ int check_group(int64_t num_tokens, int64_t topk, int64_t num_experts, bsq::Grou
     return BSQ_OK;
 }
 
+// The rows of a token_logprobs call, and how they are cut.
+int check_logprobs(int64_t num_rows, int64_t vocab, int64_t top, bsq::LogprobArgs* a) {
+    if (num_rows < 0 || num_rows > kMaxInt)
+        return fail(BSQ_ERR_INVALID_ARG, "num_rows=%lld must be in 0 .. 2^31 - 1", (long long)num_rows);
+    if (vocab > bsq::kMostVocab)
+        return fail(BSQ_ERR_UNSUPPORTED, "vocab=%lld: at most %d are provided", (long long)vocab,
+                    bsq::kMostVocab);
+    if (vocab < 1 || top < 0 || top > bsq::kMostTop || top > vocab)
+        return fail(BSQ_ERR_INVALID_ARG, "vocab=%lld must be >= 1, top=%lld in 0 .. %d and at most vocab",
+                    (long long)vocab, (long long)top, bsq::kMostTop);
+    a->rows = num_rows;
+    a->vocab = (int32_t)vocab;
+    a->top = (int32_t)top;
+    bsq::plan_logprobs(*a);
+    if (!fits((double)num_rows * a->slices, 256))
+        return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
+    return BSQ_OK;
+}
+int64_t logprobs_workspace(const bsq::LogprobArgs& a) {
+    return a.slices == 1 ? 0 : a.rows * a.slices * (8 * (int64_t)a.top + 12);
+}
+
 int check_slots(int64_t num_pages, const void* refcounts, const void* slots, int64_t n) {
     if (num_pages < 0 || num_pages > kMaxInt || n < 0 || n > kMaxInt)
         return fail(BSQ_ERR_INVALID_ARG, "num_pages=%lld and n=%lld must be in 0 .. 2^31 - 1",
@@ -688,6 +710,52 @@ int moe_group_rows(const int32_t* topk_ids, int64_t num_tokens, int64_t topk, in
     a.counts = static_cast<int32_t*>(workspace);
     a.pad = (uint32_t)pad;
     return launched(bsq::launch_group(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t token_logprobs_workspace(int64_t num_rows, int64_t vocab, int64_t top) {
+    bsq::LogprobArgs a{};
+    if (check_logprobs(num_rows, vocab, top, &a) != BSQ_OK) return -1;
+    ok();
+    return logprobs_workspace(a);
+}
+
+int token_logprobs(int dtype, const void* logits, int64_t ldl, int64_t num_rows, int64_t vocab,
+                   const int32_t* tokens, int64_t num_tokens, int64_t top, float* logprobs,
+                   float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+    bsq::LogprobArgs a{};
+    int st = check_dtype(dtype);
+    if (st == BSQ_OK) st = check_logprobs(num_rows, vocab, top, &a);
+    if (st != BSQ_OK) return st;
+    if (num_tokens < 0 || num_tokens > kMaxInt)
+        return fail(BSQ_ERR_INVALID_ARG, "num_tokens=%lld must be in 0 .. 2^31 - 1", (long long)num_tokens);
+    if (num_rows == 0) return ok();
+    if (!logits || (num_tokens > 0 && (!tokens || !logprobs)) || (top > 0 && (!top_ids || !top_logprobs)))
+        return fail(BSQ_ERR_INVALID_ARG,
+                    "null pointer (logits=%p tokens=%p logprobs=%p top_ids=%p top_logprobs=%p)", logits,
+                    tokens, logprobs, top_ids, top_logprobs);
+    if (!aligned(logits, dtype == BSQ_FP32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprobs, 4) ||
+        !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+        return fail(BSQ_ERR_INVALID_ARG, "every array must be aligned to its elements' size");
+    if (ldl < vocab)
+        return fail(BSQ_ERR_INVALID_ARG, "the row stride %lld of logits must be >= %lld", (long long)ldl,
+                    (long long)vocab);
+    const int64_t need = logprobs_workspace(a);
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+        return fail(BSQ_ERR_INVALID_ARG,
+                    "workspace (%p, %lld bytes) must be 16-byte aligned and hold %lld bytes",
+                    workspace, (long long)workspace_bytes, (long long)need);
+    a.logits = logits;
+    a.ldl = ldl;
+    a.tokens = tokens;
+    a.num_tokens = (int32_t)num_tokens;
+    a.logprobs = logprobs;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.best = static_cast<uint64_t*>(workspace);
+    if (need > 0) a.sums = reinterpret_cast<float*>(a.best + num_rows * a.slices * top);
+    return launched(bsq::launch_logprobs(a, dtype == BSQ_FP32, static_cast<hipStream_t>(stream)));
 }
 
 const char* bsq_serving_last_error(void) { return g_last_error; }

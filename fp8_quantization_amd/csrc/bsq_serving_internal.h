@@ -1,6 +1,7 @@
 // bsq_serving_internal.h -- launch interface between the host layer of
 // libbsq_serving (bsq_serving_api.cpp) and its gfx950 kernels (bsq_kv.hip,
-// bsq_pages.hip, bsq_moe.hip, bsq_rope.hip, bsq_route.hip).  Not installed.
+// bsq_pages.hip, bsq_moe.hip, bsq_rope.hip, bsq_route.hip,
+// bsq_logprobs.hip).  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -194,5 +195,22 @@ struct GroupArgs {
 };
 void plan_group(GroupArgs& a);       // tile and what follows
 hipError_t launch_group(const GroupArgs& a, hipStream_t stream);
+
+struct LogprobArgs {
+    const void* logits;
+    int64_t ldl, rows;               // elements
+    const int32_t* tokens;           // [rows][num_tokens]
+    float* logprobs;
+    float* entropy;                  // nullable
+    int32_t* top_ids;                // [rows][top]
+    float* top_logprobs;
+    float* sums;                     // [rows][slices][3], workspace of more than one slice
+    uint64_t* best;                  // [rows][slices][top], before them
+    int32_t vocab, num_tokens, top;
+    int32_t slices, per_thread;      // of a row; elements of a thread
+};
+constexpr int kMostTop = 64, kMostVocab = (1 << 19) - 8;   // 64 slices of 8192
+void plan_logprobs(LogprobArgs& a);  // slices and what follows, from rows and vocab
+hipError_t launch_logprobs(const LogprobArgs& a, bool f32, hipStream_t stream);
 
 }  // namespace bsq

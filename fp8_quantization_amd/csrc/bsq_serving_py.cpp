@@ -704,6 +704,41 @@ PyObject* group_rows(Args& a) {
     return r;
 }
 
+// logits, tokens, top, entropy, workspace, stream
+// -> (logprobs or None, entropy, top_ids, top_logprobs)
+PyObject* logprobs(Args& a) {
+    const at::Tensor& logits = logits_of(a.tensor("logits"));
+    const at::Tensor* tokens = a.tensor("tokens", true);
+    const int64_t top = a.integer("top");
+    const at::Tensor* given = a.tensor("workspace", true);
+    const CallStream stream(a);
+    const int64_t R = logits.size(0), V = logits.size(1);
+    if (tokens) {
+        if (tokens->scalar_type() != at::kInt || !tokens->is_contiguous() || tokens->dim() < 1 || tokens->dim() > 2)
+            refuse(0, "tokens must be a contiguous 1-D or 2-D GPU tensor of dtype int32");
+        if (tokens->size(0) != R)
+            refuse(BSQ_ERR_INVALID_ARG, "tokens has %lld rows; it must have %lld", (long long)tokens->size(0),
+                   (long long)R);
+    }
+    const int64_t each = !tokens ? 0 : tokens->dim() == 1 ? 1 : tokens->size(1);
+    const int64_t need = size_of(token_logprobs_workspace(R, V, top));
+    const Workspace ws(a, need ? given : nullptr, need);
+    at::Tensor own[4];
+    if (tokens) own[0] = empty(tokens->sizes(), at::kFloat, *a.device);
+    own[1] = empty({R}, at::kFloat, *a.device);
+    own[2] = empty({R, top}, at::kInt, *a.device);
+    own[3] = empty({R, top}, at::kFloat, *a.device);
+    check(token_logprobs(dtype_of(logits, "logits"), logits.data_ptr(), row_stride(logits), R, V,
+                         tokens ? tokens->data_ptr<int32_t>() : nullptr, each, top,
+                         tokens ? own[0].data_ptr<float>() : nullptr, own[1].data_ptr<float>(),
+                         own[2].data_ptr<int32_t>(), own[3].data_ptr<float>(), ws.p, ws.bytes, stream.raw));
+    PyObject* o[4] = {tokens ? stream.give(own[0], own[0]) : none(), stream.give(own[1], own[1]),
+                      stream.give(own[2], own[2]), stream.give(own[3], own[3])};
+    PyObject* r = o[0] && o[1] && o[2] && o[3] ? PyTuple_Pack(4, o[0], o[1], o[2], o[3]) : nullptr;
+    for (PyObject* p : o) Py_XDECREF(p);
+    return r;
+}
+
 #define ENTRY(name, fn) {name, (PyCFunction)(void (*)(void))entry<fn>, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY("init", init),
                            ENTRY("append", append),
@@ -717,6 +752,7 @@ PyMethodDef g_methods[] = {ENTRY("init", init),
                            ENTRY("rope", rope),
                            ENTRY("route", route),
                            ENTRY("group_rows", group_rows),
+                           ENTRY("logprobs", logprobs),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

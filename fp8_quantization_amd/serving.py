@@ -56,6 +56,9 @@ for _name, _res, *_args in (
         ("moe_route", _i32, _i32, _p, *[_i64] * 4, _i32, _p, _i64, _i64, _i32, _i32, _f32, _p, _p, _p),
         ("moe_group_rows", _i32, _p, *[_i64] * 4, _p, _p, _p, _p, _p, _i64, _p),
         ("moe_group_rows_workspace", _i64, *[_i64] * 3),
+        ("token_logprobs", _i32, _i32, _p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64,
+         _p),
+        ("token_logprobs_workspace", _i64, *[_i64] * 3),
         ("bsq_serving_last_error", ctypes.c_char_p)):
     getattr(_lib, _name).restype, getattr(_lib, _name).argtypes = _res, _args
 
@@ -245,3 +248,22 @@ def moe_group_rows(topk_ids: torch.Tensor, num_experts: int, pad: int = 128, row
     the routed row of each entry or -1)."""
     return _serving.group_rows(topk_ids, num_experts, pad, row_offsets, scales_offsets, row_indices,
                                entry_rows, workspace, stream)
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``token_logprobs`` gives: the log probabilities of the given tokens
+    (fp32, their shape; None without any), each row's entropy (fp32 [rows]) and
+    its likeliest tokens, the likeliest first (int32 and fp32 [rows, top])."""
+    logprobs: torch.Tensor | None
+    entropy: torch.Tensor
+    top_ids: torch.Tensor
+    top_logprobs: torch.Tensor
+
+
+def token_logprobs(logits: torch.Tensor, tokens=None, top: int = 0, workspace=None,
+                   stream=None) -> TokenLogprobs:
+    """Log probabilities of ``tokens`` (int32 [rows] or [rows, n]) under
+    softmax(``logits``) (BF16 or FP32 [rows, vocab]), the entropy of each row
+    and its ``top`` likeliest tokens (up to 64; equal ones by their number), in
+    one pass over the logits.  A token outside the vocabulary has -inf."""
+    return TokenLogprobs(*_serving.logprobs(logits, tokens, top, workspace, stream))

@@ -159,6 +159,36 @@ int moe_group_rows(const int32_t* topk_ids, int64_t num_tokens, int64_t topk, in
                    int64_t workspace_bytes, void* stream);
 int64_t moe_group_rows_workspace(int64_t num_tokens, int64_t topk, int64_t num_experts);
 
+/*
+ * Log probabilities under softmax(logits), with its entropy and the likeliest
+ * tokens, in one pass over the logits.
+ *
+ *   lse = log of the sum of exp(z);   logprobs = z_token - lse;
+ *   entropy = - sum of p log p;   top_ids: the `top` largest z, the largest
+ *   first, equal ones by their number, the lower first;   top_logprobs theirs.
+ *
+ * NaN counts as -inf.  A logit of +inf takes the whole probability, shared
+ * with its equals.  A row whose logits are all -inf has log probabilities of
+ * -inf and entropy 0.  A token outside the vocabulary has -inf.
+ *
+ *   dtype           of the logits [num_rows][vocab], ldl elements from a row
+ *                   to the next, aligned to their size.
+ *   vocab           1 .. 2^19 - 8 (more: BSQ_ERR_UNSUPPORTED).
+ *   tokens          int32 [num_rows][num_tokens]; logprobs fp32, as tokens;
+ *                   num_tokens 0 .. 2^31 - 1 (0: both may be NULL).
+ *   entropy         fp32 [num_rows], or NULL.
+ *   top             0 .. 64, at most vocab.  top_ids, top_logprobs: int32 /
+ *                   fp32 [num_rows][top].
+ *   workspace       16-byte aligned, token_logprobs_workspace(...) bytes (0:
+ *                   may be NULL; -1 for sizes that the call would refuse).
+ * Sums are fp32, of exp(z - the row's largest), in a fixed order.
+ */
+int token_logprobs(int dtype, const void* logits, int64_t ldl, int64_t num_rows, int64_t vocab,
+                   const int32_t* tokens, int64_t num_tokens, int64_t top, float* logprobs,
+                   float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+int64_t token_logprobs_workspace(int64_t num_rows, int64_t vocab, int64_t top);
+
 #ifdef __cplusplus
 }
 #endif

@@ -192,3 +192,47 @@ def group_rows(ids, experts, pad):
         rows.append(rows[-1] + len(g))
         scales.append(scales[-1] + (len(g) + pad - 1) // pad * pad)
     return np.array(rows), np.array(scales), index, entry
+
+
+# ------------------------------------------------------------------ log probabilities
+
+
+def logprobs(logits, tokens, top):
+    """(logprobs, entropy, top_ids, top_logprobs, and the bounds of the first, second and fourth) of
+    token_logprobs on float64 logits [rows, vocab] and tokens [rows, n].
+
+    With d = z - max, exact but for a rounding: an exponential is off by (|d| + 2) 2 U, relative,
+    and a slice's sums come to the row's by another factor of the kind; a sum of up to 32 terms a
+    thread, 6 + 2 over the threads and 6 over slices adds 46 U.  The base-2 logarithm of the
+    hardware, off by 2 U of it and U, its factor and the difference follow."""
+    R, V = logits.shape
+    z = np.where(np.isnan(logits), -np.inf, logits)
+    out = np.full(tokens.shape, -np.inf)
+    entropy, be = np.zeros(R), np.zeros(R)
+    ids = np.zeros((R, top), int)
+    best, bo, bb = np.full((R, top), -np.inf), np.zeros(tokens.shape), np.zeros((R, top))
+    for r in range(R):
+        ids[r] = np.lexsort((np.arange(V), -z[r]))[:top] if top else []
+        m = z[r].max()
+        if m == -np.inf:
+            continue
+        with np.errstate(invalid="ignore"):
+            d = np.where(z[r] == m, 0.0, z[r] - m)
+        p = np.exp(d)
+        l = p.sum()
+        p, dd = p / l, np.where(np.isfinite(d), d, 0.0)
+        off_l = (p * (np.abs(dd) + 2)).sum() * 4 * U + 46 * U
+        off_log = off_l + 6 * U * np.log(l) + 2 * U
+
+        def one(t):
+            y = d[t] - np.log(l)
+            return y, (off_log + (abs(d[t]) + abs(y)) * 2 * U + 2.0 ** -126 if np.isfinite(y) else 0.0)
+        for j, t in enumerate(tokens[r]):
+            if 0 <= t < V:
+                out[r, j], bo[r, j] = one(t)
+        for j, t in enumerate(ids[r]):
+            best[r, j], bb[r, j] = one(t)
+        entropy[r] = np.log(l) - (p * dd).sum()
+        be[r] = off_log + (p * np.abs(dd) * (4 * np.abs(dd) + 60)).sum() * U + \
+            (p * np.abs(dd)).sum() * off_l + 4 * U * (abs(entropy[r]) + np.log(l))
+    return out, entropy, ids, best, bo, be, bb

@@ -208,3 +208,44 @@ def test_reference_rows_by_hand():
     rows, scales, index, entry = R.group_rows(np.array([[2, 0], [0, 0], [-1, 3]]), 3, 4)
     assert rows.tolist() == [0, 3, 3, 4] and scales.tolist() == [0, 4, 4, 8]
     assert index.tolist() == [0, 1, 1, 0, -1, -1] and entry.tolist() == [[3, 0], [1, 2], [-1, -1]]
+
+
+# ------------------------------------------------------------------ log probabilities
+
+
+def logprobs(lib, dtype=1, z=FAKE, ldl=50000, R=4, V=50000, tokens=FAKE, n=2, top=3, lp=FAKE, H=FAKE,
+             ids=FAKE, best=FAKE, ws=FAKE, size=1 << 20):
+    return lib.token_logprobs(dtype, z, ldl, R, V, tokens, n, top, lp, H, ids, best, ws, size, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=3), UNSUPPORTED), (dict(V=(1 << 19) - 7, ldl=1 << 19), UNSUPPORTED), (dict(V=0), INVALID),
+    (dict(R=-1), INVALID), (dict(R=1 << 31), INVALID), (dict(top=-1), INVALID), (dict(top=65), INVALID),
+    (dict(V=2, top=3), INVALID), (dict(n=-1), INVALID), (dict(n=1 << 31), INVALID), (dict(z=None), INVALID),
+    (dict(tokens=None), INVALID), (dict(lp=None), INVALID), (dict(ids=None), INVALID),
+    (dict(best=None), INVALID), (dict(ldl=49999), INVALID), (dict(z=FAKE + 2), INVALID),
+    (dict(dtype=0, z=FAKE + 1), INVALID), (dict(tokens=FAKE + 2), INVALID), (dict(ws=None), INVALID),
+    (dict(ws=FAKE + 8), INVALID), (dict(size=100), INVALID), (dict(R=1 << 24), INVALID)])
+def test_logprobs_refusals(lib, kw, status):
+    assert logprobs(lib, **kw) == status
+    assert lib.bsq_serving_last_error()
+
+
+def test_logprobs_nothing_to_do_and_workspace(lib):
+    assert logprobs(lib, R=0, z=None, tokens=None) == OK
+    w = lib.token_logprobs_workspace
+    assert w(5, 2000, 4) == 0 and w(600, 8000, 4) == 0
+    assert w(1, 128000, 5) == 63 * (5 * 8 + 12) and w(2048, 128000, 20) == 2048 * 16 * (20 * 8 + 12)
+    assert w(1, 0, 0) == -1 and w(1, 5, 6) == -1 and w(1, 1 << 19, 1) == -1 and lib.bsq_serving_last_error()
+
+
+def test_reference_logprobs_by_hand():
+    z = np.log(np.array([[1.0, 3, 3, 1]]))
+    lp, H, ids, best, *bounds = R.logprobs(z, np.array([[0, 2, 4, -1]]), 3)
+    assert np.allclose(lp[0, :2], np.log([1 / 8, 3 / 8])) and lp[0, 2] == lp[0, 3] == -np.inf
+    assert ids.tolist() == [[1, 2, 0]] and np.allclose(H, -2 * (np.log(1 / 8) / 8 + np.log(3 / 8) * 3 / 8))
+    assert all(np.all(b < 1e-5) for b in bounds)
+    lp, H, ids, best, *_ = R.logprobs(np.array([[np.nan, np.inf, 0, np.inf]]), np.array([[1, 2]]), 4)
+    assert np.allclose(lp, [[-np.log(2), -np.inf]]) and np.allclose(H, np.log(2)) and ids.tolist() == [[1, 3, 2, 0]]
+    lp, H, ids, _, *_ = R.logprobs(np.full((1, 3), -np.inf), np.array([[1]]), 2)
+    assert lp[0, 0] == -np.inf and H[0] == 0 and ids.tolist() == [[0, 1]]
