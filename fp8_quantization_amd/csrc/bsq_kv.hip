@@ -40,6 +40,19 @@ __device__ __forceinline__ Seq load_seq(const KvSeqs& q, int s) {
     return r;
 }
 
+// The i-th longest of up to 64 sequences, the lower number among equals.
+__device__ __forceinline__ int longest(const KvSeqs& q, int i) {
+    const int lane = (int)threadIdx.x & 63;
+    const int32_t L = lane < q.num_seqs ? q.kv_lens[lane] : 0;
+    int before = 0;
+    for (int o = 0; o < q.num_seqs; ++o) {
+        const int32_t other = __builtin_amdgcn_readlane(L, o);
+        before += other > L || (other == L && o < lane) ? 1 : 0;
+    }
+    const uint64_t at = __ballot(before == i && lane < q.num_seqs);
+    return __ffsll((unsigned long long)at) - 1;
+}
+
 // ------------------------------------------------------------ append
 //
 // One workgroup per (page touched, head, K or V).  It reads its new tokens
@@ -387,7 +400,7 @@ __device__ __forceinline__ void move_unit(AttState<D, CB>& st, int unit) {
 // One page.  kf(j, k): the lane's 8 elements of K of token tile j and step k of
 // the contraction; vf(i, u): its 8 tokens of V of 16-element tile i and step u,
 // in units of 2^st.unit.
-template <int D, int CB, bool MASKED, class KF, class VF>
+template <int D, int CB, bool MASKED, bool LDS, class KF, class VF>
 __device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<CB, MASKED>& cols,
                                             const bf16x8 (&q)[CB][D / 32], KF kf, VF vf, uint32_t ks,
                                             uint32_t vs, int base, float c0) {
@@ -407,7 +420,7 @@ __device__ __forceinline__ void attend_page(AttState<D, CB>& st, const Columns<C
             for (int cb = 0; cb < CB; ++cb)
                 s[cb][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[cb][k], s[cb][j], 0, 0, 0);
         }
-    if constexpr (CB > 1) {
+    if constexpr (CB > 1 && LDS) {
         // K comes from LDS: six reads ahead of the products, not two (2% of a prompt)
         __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
 #pragma unroll
@@ -655,7 +668,7 @@ __device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq,
             l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Few columns (decode): a workgroup takes 16 columns of one (sequence, head)
+// Few columns (decode): a workgroup takes 16 CB columns of one (sequence, head)
 // and a run of their pages, its W waves every W-th page; their states meet
 // in LDS at the end.  ONCE: no other workgroup of the sequence reads these pages
 // (one block of columns), so they are loaded past the caches' retention.  Bound by
@@ -663,10 +676,17 @@ __device__ __forceinline__ void store_column(const AttendArgs& a, const Seq& sq,
 // (6.0 TB/s; a call 115, without ONCE 131).  Sequences that share their pages pay
 // for it, as the host does not know of them: 64 forks of one such prompt take 78 us
 // a call and would take 61, 8 of 100000 tokens 246 and 222 (apart 183 and 205).
-template <int D, int W, bool ONCE, bool MASKED>
-__global__ void __launch_bounds__(64 * W, D == 256 ? 1 : W == 4 ? 3 : 2)
+//
+// More columns than that but too few workgroups for the form below (trees of drafted tokens):
+// bound by the vector instructions, the conversion of a page's 16384 codes to 16 bits above
+// all, which two blocks of columns share (CB = 2).  16 trees of 48 tokens over 1500 .. 6000,
+// 32 heads on 8 of 128, then take 89 us a call, with one block 97.  The longest sequences go
+// first, as their workgroups come in more than one round (80 us, in the table's order 89).
+// The next page's K loaded when this one's has been multiplied, V's behind it, gave nothing (81).
+template <int D, int CB, int W, bool ONCE, bool MASKED>
+__global__ void __launch_bounds__(64 * W, D == 256 ? 1 : W == 4 && CB == 1 ? 3 : 2)
 attend_split_kernel(const AttendArgs a) {
-    __shared__ float sm[W][16], sl[W][16];
+    __shared__ float sm[W][16 * CB], sl[W][16 * CB];
     __shared__ f32x4 so[W / 2][D / 16][64];
     // heads fastest: workgroups that run at the same time read the parts of a page
     uint32_t b = blockIdx.x;
@@ -674,24 +694,27 @@ attend_split_kernel(const AttendArgs a) {
     b /= (uint32_t)a.cache.num_heads;
     const int blk = (int)(b % (uint32_t)a.col_blocks);
     b /= (uint32_t)a.col_blocks;
-    const int split = (int)(b % (uint32_t)a.splits), s = (int)(b / (uint32_t)a.splits);
+    const int split = (int)(b % (uint32_t)a.splits);
+    int s = (int)(b / (uint32_t)a.splits);
+    if constexpr (CB > 1)
+        if (a.seqs.num_seqs <= 64) s = longest(a.seqs, s);
     const Seq sq = load_seq(a.seqs, s);
-    const int cols = columns(a, sq), c0 = 16 * blk;
+    const int cols = columns(a, sq), c0 = 16 * CB * blk;
     if (c0 >= cols) return;
     const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int p0, p1;
-    const Places<MASKED> places = place_range<MASKED>(a, sq, c0, min(c0 + 16, cols) - 1, p0, p1);
+    const Places<MASKED> places = place_range<MASKED>(a, sq, c0, min(c0 + 16 * CB, cols) - 1, p0, p1);
     int from = p0, to = p1;
     split_range(a, split, from, to);
     if (split > 0 && from >= to) return;           // nor does the join look at it
     const int32_t* row = a.seqs.table + (int64_t)s * a.seqs.table_stride;
     int32_t next = from + wave < to ? row[places.page(from + wave)] : 0;
-    bf16x8 q[1][D / 32];
-    Columns<1, MASKED> v;
-    load_q<D, 1>(a, sq, kvh, c0, cols, q, v);
+    bf16x8 q[CB][D / 32];
+    Columns<CB, MASKED> v;
+    load_q<D, CB>(a, sq, kvh, c0, cols, q, v);
 
-    AttState<D, 1> st;
+    AttState<D, CB> st;
     init_state(st);
     Unit unit;
     const float cc = __builtin_fabsf(a.scale) * kLog2e;
@@ -727,7 +750,7 @@ attend_split_kernel(const AttendArgs a) {
                 for (int j = 0; j < 4; ++j)
                     vr[i][j] &= before_end(p * kKvPage + 16 * j + 4 * g, sq.L);
         }
-        attend_page<D, 1, MASKED>(
+        attend_page<D, CB, MASKED, false>(
             st, v, q,
             [&](int j, int k) {
                 const u32x4& x = kr[j][k / 2];
@@ -737,39 +760,46 @@ attend_split_kernel(const AttendArgs a) {
             p * kKvPage, cc);
     }
     // one state from the waves': their largest m, sums scaled to it
-    const float l = group_sum(st.l[0]);
-    if (g == 0) {
-        sm[wave][r] = st.m[0];
-        sl[wave][r] = l;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        const float l = group_sum(st.l[cb]);
+        if (g == 0) {
+            sm[wave][16 * cb + r] = st.m[cb];
+            sl[wave][16 * cb + r] = l;
+        }
     }
     __syncthreads();
-    float m = sm[0][r];
 #pragma unroll
-    for (int w = 1; w < W; ++w) m = fmaxf(m, sm[w][r]);
-    const float ms = m == -INFINITY ? 0.0f : m;
-    const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(st.m[0] - ms - kShift),
-                                     max(st.unit, -200));
+    for (int cb = 0; cb < CB; ++cb) {
+        const int x = 16 * cb + r;
+        float m = sm[0][x];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) st.acc[0][i] *= f;
+        for (int w = 1; w < W; ++w) m = fmaxf(m, sm[w][x]);
+        const float ms = m == -INFINITY ? 0.0f : m;
+        const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(st.m[cb] - ms - kShift),
+                                         max(st.unit, -200));
 #pragma unroll
-    for (int h = W / 2; h >= 1; h /= 2) {
-        if (wave >= h && wave < 2 * h) {
+        for (int i = 0; i < D / 16; ++i) st.acc[cb][i] *= f;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) so[wave - h][i][lane] = st.acc[0][i];
+        for (int h = W / 2; h >= 1; h /= 2) {
+            if (wave >= h && wave < 2 * h) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) so[wave - h][i][lane] = st.acc[cb][i];
+            }
+            __syncthreads();
+            if (wave < h) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) st.acc[cb][i] += so[wave][i][lane];
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (wave < h) {
+        if (wave != 0) continue;
+        float total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) st.acc[0][i] += so[wave][i][lane];
-        }
-        __syncthreads();
+        for (int w = 0; w < W; ++w)
+            total += sl[w][x] * __builtin_amdgcn_exp2f(sm[w][x] - ms - kShift);
+        store_column<D>(a, sq, kvh, c0 + x, cols, split, st.acc[cb], m, total);
     }
-    if (wave != 0) return;
-    float total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w)
-        total += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - ms - kShift);
-    store_column<D>(a, sq, kvh, c0 + r, cols, split, st.acc[0], m, total);
 }
 
 // Many columns (a prompt): the waves of a workgroup take 16 CB columns each
@@ -890,7 +920,7 @@ __global__ void __launch_bounds__(64 * W, 2) attend_rows_kernel(const AttendArgs
         if constexpr (MASKED)        // the workgroup's first columns look back further
             if (mine && page < q1 && (int64_t)page * kKvPage < a.sinks) skip = false;
         if (skip || ks_now == 256u) return;
-        attend_page<D, CB, MASKED>(
+        attend_page<D, CB, MASKED, true>(
             st, v, q, [&](int j, int k) { return kb[(8 * (k >> 1) + 2 * g + (k & 1)) * 64 + 16 * j + r]; },
             [&](int i, int u) { return vb[(2 * g + u) * D + (16 * i + r)]; }, ks_now,
             vs_now, page * kKvPage, cc);
@@ -1028,12 +1058,19 @@ void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
         else if constexpr (D == 64) attend_rows<D, 4, MASKED>(a, grid, stream);
         else if (p.wide) attend_rows<D, 8, MASKED>(a, grid, stream);
         else attend_rows<D, 4, MASKED>(a, grid, stream);
+    } else if (p.block_cols == 32) {
+        if constexpr (MASKED && D != 256) {
+            if (p.wide)
+                hipLaunchKernelGGL((attend_split_kernel<D, 2, 8, false, true>), grid, dim3(512), 0, stream, a);
+            else
+                hipLaunchKernelGGL((attend_split_kernel<D, 2, 4, false, true>), grid, dim3(256), 0, stream, a);
+        }
     } else if (p.wide) {
-        hipLaunchKernelGGL((attend_split_kernel<D, 8, false, MASKED>), grid, dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((attend_split_kernel<D, 1, 8, false, MASKED>), grid, dim3(512), 0, stream, a);
     } else if (a.col_blocks == 1) {
-        hipLaunchKernelGGL((attend_split_kernel<D, 4, true, MASKED>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attend_split_kernel<D, 1, 4, true, MASKED>), grid, dim3(256), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((attend_split_kernel<D, 4, false, MASKED>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attend_split_kernel<D, 1, 4, false, MASKED>), grid, dim3(256), 0, stream, a);
     }
     if (a.splits > 1) {
         const int64_t pairs = (int64_t)a.seqs.num_seqs * a.max_q * a.num_q_heads;
@@ -1077,8 +1114,56 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
 constexpr int64_t kSplitTarget = 2048, kSplitLeast = 16, kSplitNone = 40;
 constexpr int64_t kRowsLeast = 4;
 
+// Masked calls (sinks, trees) of more than 16 columns: a chunk of a prompt in a window, and some
+// tens of drafted tokens.  The form of many rows pays from 512 full workgroups of 128 columns on
+// (1024 rows of 16 heads on 4 of 128 in a window of 2048, of 2, 3, 4 and 8 sequences: 63, 87, 87
+// and 160 us, in blocks of 32 columns 54, 81, 105 and 192; trees of 48 tokens over 1500 .. 6000,
+// 32 heads on 8, of 4, 16 and 32: 43, 116 and 161, in blocks 38, 80 and 146).  Fewer take blocks
+// of 16 columns, or of 32 where there are kTwoBlocks of 16 (512: 36 and 38 us, 1024 of which the
+// second holds 4 columns: 124 and 102).  A tree has many pairs to join, so the pages are split
+// only until there are kMaskedGroups workgroups (25 tokens over 20000, 56 workgroups: unsplit 67
+// us, in four 31, in twenty 31; 100 over 6000, 200 workgroups: 27, in two 37, in four 34).
+constexpr int64_t kMaskedRows = 512, kTwoBlocks = 768, kMaskedGroups = 256;
+
+AttendPlan plan_masked(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
+                       int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks, bool tree) {
+    const int64_t group = num_q_heads / num_heads, cols = max_q * group;
+    const double heads = (double)num_seqs * (double)num_heads;
+    AttendPlan p{};
+    p.rows_form = cols > 64 && heads * (double)cols >= (double)kMaskedRows * kRowColumns;
+    p.block_cols = 16;
+    if (p.rows_form) {
+        p.wide = head_dim == 128 && heads * (double)(cols / kWideColumns) >= 512;
+        p.block_cols = p.wide ? kWideColumns : kRowColumns;
+    } else if (head_dim != 256 && heads * (double)((cols + 15) / 16) >= kTwoBlocks) {
+        p.block_cols = 32;
+    }
+    p.col_blocks = (int32_t)((cols + p.block_cols - 1) / p.block_cols);
+    // the pages that a block's rows see
+    int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
+    if (window > 0 && window < max_kv) {
+        const int64_t rows = tree ? max_q : std::min(max_q, p.block_cols / group + 2);
+        pages = std::min(pages, (window + rows) / kKvPage + 2 + (sinks + kKvPage - 1) / kKvPage);
+    }
+    const double blocks = heads * p.col_blocks;
+    int64_t run = std::max<int64_t>(pages, 1);
+    if (!p.rows_form && pages > kSplitNone && blocks > 0) {
+        const int64_t n = std::max<int64_t>((int64_t)(kMaskedGroups / blocks + 0.5), 1);
+        run = ((pages + n - 1) / n + kWaves - 1) / kWaves * kWaves;
+        run = std::max(run, kSplitLeast);
+    }
+    p.splits = (int32_t)std::max<int64_t>((pages + run - 1) / run, 1);
+    if (!p.rows_form) p.wide = blocks * p.splits <= 512;
+    p.threads = p.wide || (p.rows_form && head_dim == 256) ? 512 : 256;
+    p.split_pages = (int32_t)run;
+    return p;
+}
+
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
-                       int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks) {
+                       int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks, bool tree) {
+    if ((tree || (sinks > 0 && window > 0)) && max_q * (num_q_heads / num_heads) > 16)
+        return plan_masked(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks,
+                           tree);
     const int64_t cols = max_q * (num_q_heads / num_heads);
     AttendPlan p{};
     p.rows_form = cols > 64;

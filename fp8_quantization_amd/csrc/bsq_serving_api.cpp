@@ -128,7 +128,7 @@ int check_seqs(const uint32_t* row_offsets, const int32_t* kv_lens, const int32_
 
 // The query heads and sizes of an attention call, and how its work is cut.
 int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs, int64_t max_q,
-         int64_t max_kv, int64_t window, int64_t sinks, bsq::AttendPlan* p) {
+         int64_t max_kv, int64_t window, int64_t sinks, bool tree, bsq::AttendPlan* p) {
     if (num_heads < 1 || num_q_heads < 1 || num_q_heads > 65535 || num_q_heads % num_heads != 0)
         return fail(BSQ_ERR_INVALID_ARG,
                     "num_q_heads=%lld must be in 1 .. 65535 and a multiple of num_heads=%lld",
@@ -149,7 +149,8 @@ int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_s
         *p = bsq::AttendPlan{};
         return BSQ_OK;
     }
-    *p = bsq::plan_attend(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks);
+    *p = bsq::plan_attend(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks,
+                          tree);
     const double blocks = (double)num_seqs * (double)num_heads * (double)p->col_blocks * p->splits;
     const double pairs = (double)num_seqs * (double)max_q * (double)num_q_heads;
     // the join has at least a wave for each pair
@@ -265,20 +266,22 @@ int64_t kv_cache_attention_workspace(int64_t num_heads, int64_t head_dim, int64_
                                      int64_t num_seqs, int64_t num_rows, int64_t max_q,
                                      int64_t max_kv, int64_t window) {
     return kv_cache_attention_masked_workspace(num_heads, head_dim, num_q_heads, num_seqs, num_rows,
-                                               max_q, max_kv, window, 0);
+                                               max_q, max_kv, window, 0, 0);
 }
 
 int64_t kv_cache_attention_masked_workspace(int64_t num_heads, int64_t head_dim,
                                             int64_t num_q_heads, int64_t num_seqs,
                                             int64_t num_rows, int64_t max_q, int64_t max_kv,
-                                            int64_t window, int64_t sinks) {
+                                            int64_t window, int64_t sinks, int64_t mask_words) {
     bsq::AttendPlan p;
-    if (num_rows < 0 || num_rows > kMaxInt || sinks < 0 || sinks > kMaxInt) {
-        fail(BSQ_ERR_INVALID_ARG, "num_rows=%lld and sinks=%lld must be in 0 .. 2^31 - 1",
-             (long long)num_rows, (long long)sinks);
+    if (num_rows < 0 || num_rows > kMaxInt || sinks < 0 || sinks > kMaxInt || mask_words < 0) {
+        fail(BSQ_ERR_INVALID_ARG,
+             "num_rows=%lld and sinks=%lld must be in 0 .. 2^31 - 1, mask_words=%lld >= 0",
+             (long long)num_rows, (long long)sinks, (long long)mask_words);
         return -1;
     }
-    if (plan(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks, &p) != BSQ_OK)
+    if (plan(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks, mask_words > 0,
+             &p) != BSQ_OK)
         return -1;
     ok();
     return attend_workspace(p, num_rows, num_q_heads, head_dim);
@@ -317,7 +320,8 @@ int kv_cache_attention_masked(const bsq_kv_cache* cache, const void* q, int64_t 
         return fail(BSQ_ERR_INVALID_ARG, "mask_words=%lld must hold max_q=%lld bits",
                     (long long)mask_words, (long long)max_q);
     if (masks && !aligned(masks, 8)) return fail(BSQ_ERR_INVALID_ARG, "masks must be 8-byte aligned");
-    st = plan(cache->num_heads, cache->head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks, &p);
+    st = plan(cache->num_heads, cache->head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks,
+              masks != nullptr, &p);
     if (st != BSQ_OK) return st;
     if (!std::isfinite(scale)) return fail(BSQ_ERR_INVALID_ARG, "scale must be finite");
     if (num_seqs == 0 || num_rows == 0 || max_q == 0) return ok();

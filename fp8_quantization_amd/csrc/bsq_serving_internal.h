@@ -79,7 +79,7 @@ struct AttendPlan {
     int32_t threads;                 // of a workgroup
 };
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
-                       int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks);
+                       int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks, bool tree);
 hipError_t launch_kv_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
 
 struct PageArgs {

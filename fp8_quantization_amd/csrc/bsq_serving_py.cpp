@@ -364,7 +364,7 @@ PyObject* attention(Args& a) {
                    (long long)masks->size(1), (long long)max_q);
     }
     const int64_t need = size_of(kv_cache_attention_masked_workspace(
-        c.num_heads, D, Hq, t.seqs, R, max_q, max_kv, window, sinks));
+        c.num_heads, D, Hq, t.seqs, R, max_q, max_kv, window, sinks, masks ? masks->size(1) : 0));
     const Workspace ws(a, need ? given : nullptr, need);
     check(kv_cache_attention_masked(
         &c, q.data_ptr(), row_stride(q), Hq, static_cast<uint32_t*>(offsets->data_ptr()), t.lens, t.p,

@@ -50,7 +50,7 @@ for _name, _res, *_args in (
         ("moe_few_tokens_workspace", _i64, *[_i64] * 4),
         ("kv_cache_attention_masked", _i32, _p, _p, _i64, _i64, _p, _p, _p, *[_i64] * 6, _f32, _i64,
          _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p),
-        ("kv_cache_attention_masked_workspace", _i64, *[_i64] * 9),
+        ("kv_cache_attention_masked_workspace", _i64, *[_i64] * 10),
         ("qk_norm_rope", _i32, _i32, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _p, _p,
          _f32, _p, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _i64, _p),
         ("moe_route", _i32, _i32, _p, *[_i64] * 4, _i32, _p, _i64, _i64, _i32, _i32, _f32, _p, _p, _p),

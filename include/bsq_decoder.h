@@ -80,8 +80,8 @@ int qk_norm_rope(int dtype, const void* q, int64_t ldq, int64_t num_q_heads, con
  * Pages of which no row sees a token are not read, and neither are their
  * table entries.  All else as for kv_cache_attention: rows that see nothing,
  * NaN scales, pages outside the cache, sums and their order, and the
- * workspace, of kv_cache_attention_masked_workspace(...) bytes (-1 for sizes
- * that the call would refuse).
+ * workspace, of kv_cache_attention_masked_workspace(...) bytes (mask_words 0
+ * without masks; -1 for sizes that the call would refuse).
  */
 int kv_cache_attention_masked(const bsq_kv_cache* cache, const void* q, int64_t ldq,
                               int64_t num_q_heads, const uint32_t* row_offsets,
@@ -94,7 +94,7 @@ int kv_cache_attention_masked(const bsq_kv_cache* cache, const void* q, int64_t 
 int64_t kv_cache_attention_masked_workspace(int64_t num_heads, int64_t head_dim,
                                             int64_t num_q_heads, int64_t num_seqs,
                                             int64_t num_rows, int64_t max_q, int64_t max_kv,
-                                            int64_t window, int64_t sinks);
+                                            int64_t window, int64_t sinks, int64_t mask_words);
 
 /*
  * Experts of each token from a router's logits z, and their weights.

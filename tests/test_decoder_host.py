@@ -102,10 +102,14 @@ def test_masked_workspace(lib):
     w, m = lib.kv_cache_attention_workspace, lib.kv_cache_attention_masked_workspace
     for a in ((2, 128, 4, 2, 8, 1, 100000), (8, 64, 32, 3, 60, 20, 5000), (1, 256, 8, 9, 9, 1, 70000)):
         for window in (0, 100, 4000):
-            assert m(*a, window, 0) == w(*a, window)
-    assert m(2, 128, 4, 2, 8, 1, 100000, 300, 100) == 0
-    assert m(2, 128, 4, 2, 8, 1, 100000, 300, 50000) > 0
-    assert m(2, 128, 4, 2, 8, 1, 100000, 300, -1) == -1 and lib.bsq_serving_last_error()
+            assert m(*a, window, 0, 0) == w(*a, window)
+    assert m(2, 128, 4, 2, 8, 1, 100000, 300, 100, 0) == 0
+    assert m(2, 128, 4, 2, 8, 1, 100000, 300, 50000, 0) > 0
+    assert m(2, 128, 4, 2, 8, 1, 100000, 300, -1, 0) == m(2, 128, 4, 2, 8, 1, 100000, 300, 1, -1) == -1
+    assert lib.bsq_serving_last_error()
+    # trees: blocks of columns fill the chip, or their pages are split
+    assert m(8, 128, 32, 16, 700, 48, 6000, 0, 0, 1) == 0
+    assert m(8, 128, 32, 1, 25, 25, 20000, 0, 0, 1) > 0 and m(8, 128, 32, 1, 25, 25, 2000, 0, 0, 1) == 0
 
 
 def test_reference_masks():
