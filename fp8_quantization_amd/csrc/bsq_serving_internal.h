@@ -207,9 +207,10 @@ struct LogprobArgs {
     float* sums;                     // [rows][slices][3], workspace of more than one slice
     uint64_t* best;                  // [rows][slices][top], before them
     int32_t vocab, num_tokens, top;
-    int32_t slices, per_thread;      // of a row; elements of a thread
+    int32_t slices, per_thread;      // of a row; elements of a thread and chunk
+    int32_t chunks;                  // of a slice
 };
-constexpr int kMostTop = 64, kMostVocab = (1 << 19) - 8;   // 64 slices of 8192
+constexpr int kMostTop = 64, kMostVocab = (1 << 19) - 8;
 void plan_logprobs(LogprobArgs& a);  // slices and what follows, from rows and vocab
 hipError_t launch_logprobs(const LogprobArgs& a, bool f32, hipStream_t stream);
 

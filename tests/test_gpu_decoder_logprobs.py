@@ -171,3 +171,56 @@ def test_refusals_of_the_binding(bsq):  # noqa: F811
         args.update(kw)
         with pytest.raises(err):
             bsq.token_logprobs(**args)
+
+
+@pytest.mark.parametrize("vocab,rows", [(300, 2), (40000, 2), (40000, 700)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_masked_vocabularies(bsq, vocab, rows, dtype):  # noqa: F811
+    """Most of the vocabulary masked, by -inf, by the type's lowest number or by a large one: fewer
+    tokens left than are asked for, one, none; the left ones early, late and in between."""
+    x, t = random(rows, vocab, dtype)
+    low = torch.finfo(dtype).min
+    keep = [[0, 1, 2], [vocab - 1], [5, vocab // 2, vocab - 3], [], list(range(100, 130)),
+            list(range(0, vocab, 97))]
+    cases = [(m, k) for m in (-float("inf"), low, -1e9, -2e4) for k in keep]
+    y = torch.empty((len(cases), vocab), device="cuda", dtype=dtype)
+    for i, (m, k) in enumerate(cases):
+        y[i] = m
+        if k:
+            y[i, k] = x[0, k]
+    if rows > 2:                     # long slices, several chunks each
+        y = y.repeat(rows // len(cases) + 1, 1)
+    t = np.tile([[0, 1, vocab - 1]], (y.shape[0], 1))
+    got = bsq.token_logprobs(y, i32(t), top=20)
+    want = check(bsq, y[:len(cases)], t[:len(cases)], 20)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for r in range(0, y.shape[0], len(cases)):
+            part = g[r:r + len(cases)]
+            assert torch.equal(part, g[:len(part)])
+        assert torch.allclose(g[:len(cases)].float(), w.float(), rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("shift", [1e3, -1e3, 1.5e4, -1.5e4, 1.7e4, -1.7e4, 1e6, -1e6, 1e37])
+def test_shifted_logits(bsq, shift):  # noqa: F811
+    """What is added to all logits is not lost."""
+    x, t = random(3, 30000, torch.float32)
+    check(bsq, x + shift, t, 12)
+
+
+@pytest.mark.parametrize("vocab", [20000, 130000])
+def test_ties_of_many_in_long_slices(bsq, vocab):  # noqa: F811
+    """More equal numbers than are ranked at once, beside larger ones, in slices of several chunks."""
+    x = torch.zeros((2100, vocab), device="cuda", dtype=torch.bfloat16)
+    rng = np.random.default_rng(3)
+    for r in range(4):
+        at = rng.choice(vocab, 3 + 5 * r, replace=False)
+        x[r, torch.tensor(at, device="cuda")] = torch.tensor(rng.integers(1, 4, len(at)), device="cuda").to(x.dtype)
+    x[4] = torch.linspace(-3, 3, vocab, device="cuda").to(x.dtype)
+    t = rng.integers(0, vocab, (2100, 1))
+    got = bsq.token_logprobs(x, i32(t), top=16)
+    torch.cuda.synchronize()
+    _, _, ids, best, _, _, bb = R.logprobs(x[:5].double().cpu().numpy(), t[:5], 16)
+    assert np.array_equal(got.top_ids[:5].cpu().numpy(), ids)
+    assert np.all(np.abs(got.top_logprobs[:5].double().cpu().numpy() - best) <= bb)
+    assert bool((got.top_ids[5:] == torch.arange(16, device="cuda")).all())
