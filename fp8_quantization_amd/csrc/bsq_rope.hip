@@ -3,12 +3,15 @@
 //
 // A lane holds 8 consecutive elements of a head, L lanes a head, so every load
 // and store is whole 16-byte pieces and a wave's are consecutive.  The angles of
-// a row are the same for all of its heads: a wave computes its lanes' cosines
-// and sines once and takes several heads with them, one step (64 / L heads)
+// a row are the same for all of its heads: a wave finds their cosines and sines
+// once, a lane each, and takes several heads with them, one step (64 / L heads)
 // after the other, the next step's elements being on their way.  The norm is a
 // sum over the L lanes; with halves a pair's other element is 8 elements of
 // another lane (rotary_dim being a multiple of 16), with neighbours it is the
-// lane's own.
+// lane's own.  Bound by the bytes: 16384 rows of 32 + 8 heads of 128 in BF16, 336
+// MB read and written, take 71 us (4.7 TB/s; a copy reaches 5.2).  With the
+// angles found by every lane for its own elements and lanes exchanged through
+// LDS it took 85.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -54,28 +57,44 @@ __device__ __forceinline__ float inv_sqrt(float v) {
     return __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v) * (tiny ? 0x1p30f : 1.0f);
 }
 
-// The sum over the L lanes of a head, in each of them.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+// The number of lane ^ 16.
+__device__ __forceinline__ float across_rows(float v) {
+    const uint32_t b = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    return __uint_as_float(threadIdx.x & 16 ? a[0] : a[1]);
+}
+// The sum over the L lanes of a head, in each of them: lanes ^ 1, ^ 2, mirrors of 8 and of 16.
 template <int L>
 __device__ __forceinline__ float head_sum(float v) {
-#pragma unroll
-    for (int off = L / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    v += moved<0xB1>(v);
+    v += moved<0x4E>(v);
+    v += moved<0x141>(v);
+    if constexpr (L >= 16) v += moved<0x140>(v);
+    if constexpr (L == 32) v += across_rows(v);
     return v;
+}
+// The number of lane ^ L / 2.
+template <int L>
+__device__ __forceinline__ float of_other_half(float v) {
+    if constexpr (L == 8) return moved<0x1B>(moved<0x141>(v));
+    else if constexpr (L == 16) return moved<0x128>(v);
+    else return across_rows(v);
 }
 
 template <bool F32>
 struct Piece {
     u32x4 w[F32 ? 2 : 1];            // 8 elements
 };
-template <bool F32>
+template <bool F32, bool ONCE>
 __device__ __forceinline__ Piece<F32> load_piece(const void* x, int64_t at) {
     Piece<F32> p;
-    if constexpr (F32) {
-        const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(x) + at);
-        p.w[0] = s[0];
-        p.w[1] = s[1];
-    } else {
-        p.w[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at);
-    }
+    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const char*>(x) + at * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) p.w[i] = ONCE ? __builtin_nontemporal_load(s + i) : s[i];
     return p;
 }
 template <bool F32>
@@ -87,7 +106,10 @@ __device__ __forceinline__ void unpack(const Piece<F32>& p, float (&y)[8]) {
     }
 }
 
-template <int L, bool F32, bool PAIRS>
+// How pairs lie: anywhere in two halves, in the two halves of all L lanes, or beside each other.
+enum Pairs { kHalves, kWhole, kNeighbours };
+
+template <int L, bool F32, Pairs PAIRS, bool ONCE>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int H = 64 / L;                            // heads of a step
     const int lane = (int)threadIdx.x & 63, l = lane % L, sub = lane / L;
@@ -97,25 +119,6 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     const int first = (int)(wave % a.parts) * a.steps, end = min(first + a.steps, a.all_steps);
     const int d = 8 * l;
     const bool on = d < a.head_dim;
-
-    // positions * inv_freq in turns, 1 / (2 pi) of it; the first of a pair takes the sine off
-    constexpr int N = PAIRS ? 4 : 8;
-    float cs[N], sn[N];
-    const bool turned = d < a.rotary_dim;
-    const int half = a.rotary_dim / 2;
-    const bool low = d < half;
-    const double pos = a.rotary_dim > 0 ? (double)a.positions[row] * 0.15915494309189533576888 : 0.0;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        cs[e] = 1.0f;
-        sn[e] = 0.0f;
-        if (turned) {
-            const int i = PAIRS ? d / 2 + e : (low ? d : d - half) + e;
-            sincos_turns(pos * a.inv_freq[i], sn[e], cs[e]);
-            if (!PAIRS && low) sn[e] = -sn[e];
-        }
-    }
-    const int other = PAIRS || !turned ? lane : low ? lane + half / 8 : lane - half / 8;
 
     // step -> segment (q, k or v) and its first head
     auto place = [&](int step, int& seg, int& head) {
@@ -129,12 +132,39 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
         place(step, seg, head);
         Piece<F32> p{};
         if (on && head < a.heads[seg])
-            p = load_piece<F32>(a.x[seg], row * a.ldx[seg] + (int64_t)head * a.head_dim + d);
+            p = load_piece<F32, ONCE>(a.x[seg], row * a.ldx[seg] + (int64_t)head * a.head_dim + d);
         return p;
     };
+    // Each lane finds one angle of the row (or two), and takes those of its elements from the
+    // others; the first of a pair takes the sine off.
+    constexpr int N = PAIRS == kNeighbours ? 4 : 8;
+    __shared__ f32x4 turns[kWaves][2][32];
+    float cs[N], sn[N];
+    const bool turned = d < a.rotary_dim;
+    const int half = a.rotary_dim / 2;
+    const bool low = d < half;
+    const Piece<F32> early = fetch(first);
+    if (half > 0) {
+        const double pos = (double)a.positions[row] * 0.15915494309189533576888;   // 1 / (2 pi)
+        float* all = reinterpret_cast<float*>(turns[threadIdx.x >> 6]);
+        for (int i = lane; i < half; i += 64) sincos_turns(pos * a.inv_freq[i], all[i], all[128 + i]);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (turned) {
+            const int i = PAIRS == kNeighbours ? d / 2 : low ? d : d - half;   // a multiple of 4
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float s = turns[threadIdx.x >> 6][0][i / 4 + e / 4][e % 4];
+                sn[e] = PAIRS != kNeighbours && low ? -s : s;
+                cs[e] = turns[threadIdx.x >> 6][1][i / 4 + e / 4][e % 4];
+            }
+        }
+    }
+    const int other = PAIRS != kHalves || !turned ? lane : low ? lane + half / 8 : lane - half / 8;
+
     float w[8];
     int weights_of = -1;
-    Piece<F32> next = fetch(first);
+    Piece<F32> next = early;
     for (int step = first; step < end; ++step) {
         int seg, head;
         place(step, seg, head);
@@ -160,7 +190,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if constexpr (PAIRS) {
+                if constexpr (PAIRS == kWhole) {
+                    o[e] = __builtin_fmaf(y[e], cs[e], of_other_half<L>(y[e]) * sn[e]);
+                } else if constexpr (PAIRS == kNeighbours) {
                     const float t = e % 2 ? sn[e / 2] : -sn[e / 2];
                     o[e] = __builtin_fmaf(y[e], cs[e / 2], y[e ^ 1] * t);
                 } else {
@@ -184,26 +216,37 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     }
 }
 
-// Steps of a wave: all of a row's where that gives waves enough for the CUs, else fewer, down to one.
+// Steps of a wave: all of a row's where that gives waves enough for the CUs, else fewer, down to one
+// (16384 rows of 40 heads: 76 us with 10 steps a wave, 79 with five).
 constexpr int64_t kWavesWanted = 4096;
+// Inputs larger than the memory-side cache are read past the caches (336 MB read and written: 71
+// us, through them 77); smaller ones may lie there still (84 MB: 27 and 21).
+constexpr int64_t kCached = 256 << 20;
 
-template <int L, bool F32, bool PAIRS>
+template <int L, bool F32, Pairs PAIRS>
 void rope(const RopeArgs& a, hipStream_t stream) {
-    const int64_t waves = a.num_rows * a.parts;
-    hipLaunchKernelGGL((qk_norm_rope_kernel<L, F32, PAIRS>),
-                       dim3((uint32_t)((waves + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream, a);
+    const dim3 grid((uint32_t)((a.num_rows * a.parts + kWaves - 1) / kWaves));
+    if (a.once)
+        hipLaunchKernelGGL((qk_norm_rope_kernel<L, F32, PAIRS, true>), grid, dim3(kThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL((qk_norm_rope_kernel<L, F32, PAIRS, false>), grid, dim3(kThreads), 0, stream, a);
+}
+template <int L, bool F32>
+void rope_of(const RopeArgs& a, bool pairs, hipStream_t stream) {
+    if (pairs) rope<L, F32, kNeighbours>(a, stream);
+    else if (a.rotary_dim == 8 * L) rope<L, F32, kWhole>(a, stream);
+    else rope<L, F32, kHalves>(a, stream);
 }
 template <int L>
 void rope_of(const RopeArgs& a, bool f32, bool pairs, hipStream_t stream) {
-    if (f32) pairs ? rope<L, true, true>(a, stream) : rope<L, true, false>(a, stream);
-    else pairs ? rope<L, false, true>(a, stream) : rope<L, false, false>(a, stream);
+    f32 ? rope_of<L, true>(a, pairs, stream) : rope_of<L, false>(a, pairs, stream);
 }
 
 int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
 
 }  // namespace
 
-void plan_rope(RopeArgs& a) {
+void plan_rope(RopeArgs& a, bool f32) {
     const int heads = 64 / lanes_of(a.head_dim);
     a.all_steps = 0;
     for (int s = 0; s < 3; ++s) {
@@ -213,6 +256,8 @@ void plan_rope(RopeArgs& a) {
     const int64_t all = a.num_rows * a.all_steps;
     a.steps = (int32_t)std::min<int64_t>(std::max<int64_t>(all / kWavesWanted, 1), a.all_steps);
     a.parts = (a.all_steps + a.steps - 1) / a.steps;
+    const int64_t width = (int64_t)(a.heads[0] + a.heads[1] + a.heads[2]) * a.head_dim;
+    a.once = (double)a.num_rows * width * (f32 ? 6 : 4) > (double)kCached;
 }
 
 hipError_t launch_rope(const RopeArgs& a, bool f32, bool pairs, hipStream_t stream) {

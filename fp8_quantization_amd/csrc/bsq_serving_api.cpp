@@ -614,7 +614,7 @@ int qk_norm_rope(int dtype, const void* q, int64_t ldq, int64_t num_q_heads, con
     a.inv_dim = 1.0f / (float)head_dim;
     a.head_dim = (int32_t)head_dim;
     a.rotary_dim = (int32_t)rotary_dim;
-    bsq::plan_rope(a);
+    bsq::plan_rope(a, dtype == BSQ_FP32);
     if (!fits((double)num_rows * a.parts, 64) || num_rows * a.parts > kMaxInt - 4)
         return fail(BSQ_ERR_INVALID_ARG, "problem too large for one launch");
     return launched(bsq::launch_rope(a, dtype == BSQ_FP32, interleaved != 0,

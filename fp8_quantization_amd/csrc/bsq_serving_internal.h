@@ -158,8 +158,9 @@ struct RopeArgs {
     int32_t head_dim, rotary_dim;
     int32_t seg_steps[3], all_steps; // steps (of as many heads as a wave takes at once) of a row
     int32_t steps, parts;            // of a wave; waves of a row
+    bool once;                       // loads past the caches
 };
-void plan_rope(RopeArgs& a);         // seg_steps and what follows, from the sizes
+void plan_rope(RopeArgs& a, bool f32);   // seg_steps and what follows, from the sizes
 hipError_t launch_rope(const RopeArgs& a, bool f32, bool pairs, hipStream_t stream);
 
 struct RouteArgs {

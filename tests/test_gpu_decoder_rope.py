@@ -162,3 +162,20 @@ def test_refusals_of_the_binding(bsq):  # noqa: F811
         args.update(kw)
         with pytest.raises(err):
             bsq.qk_norm_rope(**args)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_inputs_past_the_caches_size(bsq, dtype, interleaved):  # noqa: F811
+    """More bytes than the memory-side cache holds are read another way: the same bits as in parts."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows, cut = 12000, 7000
+    q = torch.randn((rows, 32, 128), generator=g, device="cuda").to(dtype)
+    k = torch.randn((rows, 12, 128), generator=g, device="cuda").to(dtype)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    f, w = torch.tensor(1000.0 ** (-np.arange(64) / 64), device="cuda"), torch.ones(128, device="cuda")
+    a = bsq.qk_norm_rope(q, k, pos, f, q_weight=w, k_weight=w, interleaved=interleaved)
+    for lo, hi in ((0, cut), (cut, rows)):
+        b = bsq.qk_norm_rope(q[lo:hi], k[lo:hi], pos[lo:hi], f, q_weight=w, k_weight=w, interleaved=interleaved)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0][lo:hi], b[0]) and torch.equal(a[1][lo:hi], b[1])
