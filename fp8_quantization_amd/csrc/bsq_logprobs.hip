@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "bsq_serving_internal.h"
+#include "bsq_wave.h"
 
 namespace bsq {
 namespace {
@@ -24,50 +25,10 @@ constexpr int kThreads = 256, kWaves = 4;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kMostFound = 2048;     // elements that are ranked at most
 
-__device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t key) {
-    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
-}
 // A number and a place in the order of the answer: the larger number, then the lower place.
 // 0: nothing.
 __device__ __forceinline__ uint64_t entry_of(float x, int place) {
     return (uint64_t)key_of(x) << 32 | (uint32_t)~place;
-}
-
-// The wave's results in every lane: rotations by 8, 4, 2, 1 within the rows of 16 lanes, then
-// across them.
-template <int CTRL>
-__device__ __forceinline__ uint32_t turned(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-template <class F>
-__device__ __forceinline__ uint32_t wave_all(uint32_t v, F f) {
-    v = f(v, turned<0x128>(v));
-    v = f(v, turned<0x124>(v));
-    v = f(v, turned<0x122>(v));
-    v = f(v, turned<0x121>(v));
-    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = f(a[0], a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return f(b[0], b[1]);
-}
-__device__ __forceinline__ float wave_max(float v) {
-    return __uint_as_float(wave_all(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-    }));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-    return __uint_as_float(wave_all(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-    }));
-}
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-    const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-    const uint32_t hi = wave_all((uint32_t)(v >> 32), larger);
-    return (uint64_t)hi << 32 | wave_all((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u, larger);
 }
 
 // exp(x - m); 1 where both are the same infinity, 0 for x = -inf.

@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "bsq_serving_internal.h"
+#include "bsq_wave.h"
 
 namespace bsq {
 namespace {
@@ -19,47 +20,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // A wave a token, expert e in lane e % 64 of register e / 64.  The topk largest
 // are taken one after the other by the wave's largest key, a number's bits in
 // an order of unsigned integers (0: not to be chosen).
-
-__device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ uint64_t key_of(double x) {
-    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
-    return b >> 63 ? ~b : b | 1ull << 63;
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
-}
-// The largest of the wave's numbers, in every lane: rotations within the rows of 16 lanes, then
-// across them.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = dpp_max<0x128>(v);
-    v = dpp_max<0x124>(v);
-    v = dpp_max<0x122>(v);
-    v = dpp_max<0x121>(v);
-    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = max(a[0], a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return __builtin_amdgcn_readfirstlane(max(b[0], b[1]));
-}
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-    const uint32_t hi = wave_max((uint32_t)(v >> 32));
-    const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-    return (uint64_t)hi << 32 | lo;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-    return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-    return v;
-}
 
 // A logit; NaN counts as -inf.
 template <bool F32>
@@ -82,16 +42,48 @@ __device__ __forceinline__ float share(float x, float top) {
     return x == top ? 1.0f : __builtin_amdgcn_exp2f((x - top) * kLog2e);
 }
 
-// The topk largest keys, the lowest expert among equals: lane j gets the j-th's expert.
-template <int REGS, class K>
-__device__ __forceinline__ int choose(K (&key)[REGS], int topk) {
-    const int lane = (int)threadIdx.x & 63;
+// Whether what 32 bits put in this order is in it: a before b, which are off by `off` at most
+// between them, and by a rounding each.
+__device__ __forceinline__ bool surely(float a, float b, float off) {
+    if (b == -INFINITY) return a > -INFINITY;
+    return a - b > off + (__builtin_fabsf(a) + __builtin_fabsf(b)) * 0x1p-21f;
+}
+
+// A lane's choice: an expert and its logit, -inf where it has no weight.
+struct Choice {
     int id = 0;
-    for (int j = 0; j < topk; ++j) {
+    float z = -INFINITY;
+};
+__device__ __forceinline__ float of_lane(float v, int lane) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double of_lane(double v, int lane) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// The topk largest keys, the lowest expert among equals: lane j gets the j-th.  x: the logits.
+// CHECK: ok becomes false where the order of those and the next is not sure.
+template <int REGS, bool CHECK, class K>
+__device__ __forceinline__ Choice choose(K (&key)[REGS], const float (&x)[REGS],
+                                         const float (&bias)[REGS], int topk, float off, bool& ok) {
+    const int lane = (int)threadIdx.x & 63;
+    Choice c;
+    float last = INFINITY;
+    for (int j = 0; j < topk + (CHECK ? 1 : 0); ++j) {
         K best = key[0];
 #pragma unroll
         for (int k = 1; k < REGS; ++k) best = max(best, key[k]);
         best = wave_max(best);
+        if constexpr (CHECK) {
+            if (best == 0) break;    // no more to be chosen
+            const float v = value_of(best);
+            if (j > 0) ok = ok && surely(last, v, off);
+            last = v;
+            if (j == topk) break;
+        }
         bool taken = false;
 #pragma unroll
         for (int k = 0; k < REGS; ++k) {
@@ -99,18 +91,23 @@ __device__ __forceinline__ int choose(K (&key)[REGS], int topk) {
             if (!taken && at) {
                 taken = true;
                 const int l = __ffsll((unsigned long long)at) - 1;
-                if (lane == j) id = 64 * k + l;
+                const float z = of_lane(bias[k] > -INFINITY ? x[k] : -INFINITY, l);
+                if (lane == j) {
+                    c.id = 64 * k + l;
+                    c.z = z;
+                }
                 if (lane == l) key[k] = 0;
             }
         }
     }
-    return id;
+    return c;
 }
 
 // Closes the groups that are not kept: their experts' keys become 0.  Lane g * P + i looks at
-// every P-th expert of group g; `all`: the wave's numbers in LDS.
-template <int REGS, class K, class F>
-__device__ __forceinline__ void close_groups(const RouteArgs& a, K (&key)[REGS], const F (&c)[REGS], F* all) {
+// every P-th expert of group g; `all`: the wave's numbers in LDS.  CHECK as above.
+template <int REGS, bool CHECK, class K, class F>
+__device__ __forceinline__ void close_groups(const RouteArgs& a, K (&key)[REGS], const F (&c)[REGS], F* all,
+                                             float off, bool& ok) {
     const int lane = (int)threadIdx.x & 63;
 #pragma unroll
     for (int k = 0; k < REGS; ++k)
@@ -124,8 +121,8 @@ __device__ __forceinline__ void close_groups(const RouteArgs& a, K (&key)[REGS],
             two = v > one ? one : v > two ? v : two;
             one = v > one ? v : one;
         }
-    for (int off = P / 2; off >= 1; off >>= 1) {
-        const F o1 = __shfl_xor(one, off), o2 = __shfl_xor(two, off);
+    for (int by = P / 2; by >= 1; by >>= 1) {
+        const F o1 = __shfl_xor(one, by), o2 = __shfl_xor(two, by);
         two = o1 > one ? (one > o2 ? one : o2) : (two > o1 ? two : o1);
         one = o1 > one ? o1 : one;
     }
@@ -134,10 +131,16 @@ __device__ __forceinline__ void close_groups(const RouteArgs& a, K (&key)[REGS],
     // how many groups go before this one
     int before = 0;
     for (int o = 0; o < a.groups; ++o) {
-        const F v = __shfl(score, o * P);
+        const F v = of_lane(score, o * P);
         before += v > score || (v == score && o < g) ? 1 : 0;
     }
-    const uint64_t kept = __ballot(g < a.groups && lane % P == 0 && before < a.keep);
+    const bool group = g < a.groups && lane % P == 0, keep = group && before < a.keep;
+    const uint64_t kept = __ballot(keep);
+    if constexpr (CHECK) {           // the lowest kept, the highest not
+        const float in = -wave_max(keep ? -score : -INFINITY);
+        const float out = wave_max(group && !keep ? score : -INFINITY);
+        ok = a.keep == a.groups || surely(in, out, 2.0f * off);
+    }
 #pragma unroll
     for (int k = 0; k < REGS; ++k) {
         const int e = 64 * k + lane;
@@ -147,13 +150,9 @@ __device__ __forceinline__ void close_groups(const RouteArgs& a, K (&key)[REGS],
     __builtin_amdgcn_wave_barrier();
 }
 
-// The weights of a token's experts, lane j's being `id`.
-template <bool F32, int REGS>
-__device__ __forceinline__ float weight_of(const RouteArgs& a, int64_t token, int id, const float (&x)[REGS]) {
-    const int lane = (int)threadIdx.x & 63;
-    const bool mine = lane < a.topk;
-    float z = -INFINITY;
-    if (mine && bias_of(a, id) > -INFINITY) z = logit<F32>(a, token, id);
+// The weights of a token's experts, lane j's having the logit z (past topk -inf).
+template <int REGS>
+__device__ __forceinline__ float weight_of(const RouteArgs& a, float z, const float (&x)[REGS]) {
     float s, sum;
     if (a.sigmoid) {
         // where every chosen logit is negative their scores are taken relative to the largest's
@@ -184,7 +183,8 @@ __device__ __forceinline__ float weight_of(const RouteArgs& a, int64_t token, in
 
 // The choice by c in 64 bits (of experts by the logits where there is no bias).
 template <int REGS>
-__device__ __forceinline__ int choose_exactly(const RouteArgs& a, const float (&x)[REGS], double* all) {
+__device__ __forceinline__ Choice choose_exactly(const RouteArgs& a, const float (&x)[REGS],
+                                                 const float (&bias)[REGS], double* all) {
     const int lane = (int)threadIdx.x & 63;
     double s[REGS], sum = 0.0;
     float top = x[0];
@@ -207,23 +207,66 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, const float (&
 #pragma unroll
     for (int k = 0; k < REGS; ++k) {
         const int e = 64 * k + lane;
-        const float b = e < a.experts ? bias_of(a, e) : -INFINITY;
+        const float b = bias[k];
         s[k] = !(x[k] > -INFINITY) || b == -INFINITY ? -INFINITY : (a.sigmoid ? s[k] : s[k] / sum) + b;
         key[k] = e < a.experts ? key_of(a.bias ? s[k] : (double)x[k]) : 0;
     }
-    if (a.groups > 1) close_groups(a, key, s, all);
-    return choose(key, a.topk);
+    bool ok;
+    if (a.groups > 1) close_groups<REGS, false>(a, key, s, all, 0.0f, ok);
+    return choose<REGS, false>(key, x, bias, a.topk, 0.0f, ok);
+}
+
+// The choice by c in 32 bits; ok: it is that of 64.
+//   sigmoid: the exponential of x is off by 1.5 |x| + 2 in units of 2^-24 of it, 1 + t and the
+//     reciprocal by 3: with s (1 - s) |x| < 0.23 and s (1 - s) <= 1/4, s by less than 4.  Two of
+//     them: 2^-21; four times that is taken.
+//   softmax: a share e^-d of the largest is off by (2.5 d + 2) of it, the sum by the shares' mean of
+//     that (at most 2.5 log 1024 + 2) and 22 for its additions, the quotient by 2: s by less than
+//     50 in units of 2^-24 of the largest s.  Two of them: 2^-17 of it; twice that is taken.
+template <int REGS>
+__device__ __forceinline__ Choice choose_nearly(const RouteArgs& a, const float (&x)[REGS],
+                                                const float (&bias)[REGS], float* all, bool& ok) {
+    const int lane = (int)threadIdx.x & 63;
+    float s[REGS], off = 0x1p-19f, scale = 1.0f;
+    if (!a.sigmoid) {
+        float top = x[0], sum = 0.0f;
+#pragma unroll
+        for (int k = 1; k < REGS; ++k) top = fmaxf(top, x[k]);
+        top = wave_max(top);
+#pragma unroll
+        for (int k = 0; k < REGS; ++k) {
+            s[k] = share(x[k], top);
+            sum += s[k];
+        }
+        scale = __builtin_amdgcn_rcpf(wave_sum(sum));
+        off = scale * 0x1p-16f;
+    }
+    uint32_t key[REGS];
+#pragma unroll
+    for (int k = 0; k < REGS; ++k) {
+        const int e = 64 * k + lane;
+        const float b = bias[k];
+        if (a.sigmoid) s[k] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[k] * -kLog2e));
+        s[k] = !(x[k] > -INFINITY) || b == -INFINITY ? -INFINITY : s[k] * scale + b;
+        key[k] = e < a.experts ? key_of(a.bias ? s[k] : x[k]) : 0u;
+    }
+    ok = true;
+    if (a.groups > 1) close_groups<REGS, true>(a, key, s, all, off, ok);
+    if (a.bias) return choose<REGS, true>(key, x, bias, a.topk, off, ok);
+    return choose<REGS, false>(key, x, bias, a.topk, off, ok);
 }
 
 // Without a bias, and with groups by their best, c goes by the logit.
 template <int REGS>
-__device__ __forceinline__ int choose_logits(const RouteArgs& a, const float (&x)[REGS], float* all) {
+__device__ __forceinline__ Choice choose_logits(const RouteArgs& a, const float (&x)[REGS],
+                                                const float (&bias)[REGS], float* all) {
     const int lane = (int)threadIdx.x & 63;
     uint32_t key[REGS];
+    bool ok;
 #pragma unroll
     for (int k = 0; k < REGS; ++k) key[k] = 64 * k + lane < a.experts ? key_of(x[k]) : 0u;
-    if (a.groups > 1) close_groups(a, key, x, all);
-    return choose(key, a.topk);
+    if (a.groups > 1) close_groups<REGS, false>(a, key, x, all, 0.0f, ok);
+    return choose<REGS, false>(key, x, bias, a.topk, 0.0f, ok);
 }
 
 template <int REGS, bool F32>
@@ -233,16 +276,24 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t token = (int64_t)blockIdx.x * kWaves + wave;
     if (token >= a.tokens) return;
-    float x[REGS];
+    float x[REGS], bias[REGS];
 #pragma unroll
-    for (int k = 0; k < REGS; ++k)
-        x[k] = 64 * k + lane < a.experts ? logit<F32>(a, token, 64 * k + lane) : -INFINITY;
-    const int id = !a.bias && (a.groups == 1 || a.group_top == 1 || a.group_size == 1)
-                       ? choose_logits(a, x, reinterpret_cast<float*>(all[wave]))
-                       : choose_exactly(a, x, all[wave]);
-    const float w = weight_of<F32>(a, token, id, x);
+    for (int k = 0; k < REGS; ++k) {
+        const int e = 64 * k + lane;
+        x[k] = e < a.experts ? logit<F32>(a, token, e) : -INFINITY;
+        bias[k] = e < a.experts ? bias_of(a, e) : -INFINITY;
+    }
+    Choice c;
+    if (!a.bias && (a.groups == 1 || a.group_top == 1 || a.group_size == 1)) {
+        c = choose_logits(a, x, bias, reinterpret_cast<float*>(all[wave]));
+    } else {
+        bool ok;
+        c = choose_nearly(a, x, bias, reinterpret_cast<float*>(all[wave]), ok);
+        if (!ok) c = choose_exactly(a, x, bias, all[wave]);
+    }
+    const float w = weight_of(a, c.z, x);
     if (lane < a.topk) {
-        a.ids[token * a.topk + lane] = id;
+        a.ids[token * a.topk + lane] = c.id;
         a.weights[token * a.topk + lane] = w;
     }
 }
@@ -260,11 +311,12 @@ void route(const RouteArgs& a, bool f32, hipStream_t stream) {
 // its waves a part of it; a wave goes through its part 64 entries at a time.
 // Which of the 64 name the same expert is found by a ballot for each bit of the
 // number, so an entry's rank among them is a count of lanes, and no order of
-// atomics takes part.  Few entries are one workgroup's; more are counted by a
-// kernel before, a tile a workgroup, whose counts every workgroup then adds up
-// for its own place.
+// atomics takes part.  Few entries are one workgroup's; of more, a first kernel
+// finds the ranks within the tiles and the tiles' counts, and a second adds up the
+// counts for each tile and places the entries.
 
 constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
+constexpr int kKept = 8;             // steps of a wave whose entries stay in registers
 
 // The lanes whose number is the same.
 __device__ __forceinline__ uint64_t same_lanes(int v, int bits) {
@@ -281,73 +333,16 @@ __device__ __forceinline__ int expert_of(const GroupArgs& a, int64_t i, int64_t 
     return id >= 0 && id < a.experts ? id : a.experts;      // experts: no expert
 }
 
-__global__ void __launch_bounds__(kSortThreads) group_count_kernel(const GroupArgs a) {
-    __shared__ int32_t count[kMoeMaxExperts + 1];
-    for (int e = (int)threadIdx.x; e <= a.experts; e += kSortThreads) count[e] = 0;
-    __syncthreads();
-    const int64_t first = (int64_t)blockIdx.x * a.tile, end = min(first + a.tile, a.entries);
-    for (int64_t i = first + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&count[expert_of(a, i, end)], 1);
-    __syncthreads();
-    for (int e = (int)threadIdx.x; e < a.experts; e += kSortThreads)
-        a.counts[(int64_t)blockIdx.x * a.experts + e] = count[e];
-}
-
-template <bool ALONE>
-__global__ void __launch_bounds__(kSortThreads) group_rows_kernel(const GroupArgs a) {
-    // per wave and expert: its entries, then where its next one goes
-    __shared__ volatile int32_t place[kSortWaves][kMoeMaxExperts + 1];
-    __shared__ int32_t total[kMoeMaxExperts], before[kMoeMaxExperts];
-    __shared__ uint32_t sums[2][kSortWaves];
-    const int tid = (int)threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t first = (int64_t)blockIdx.x * a.tile, tile_end = min(first + a.tile, a.entries);
-    const int64_t part = a.tile / kSortWaves;
-    const int64_t from = first + wave * part, to = min(from + part, tile_end);
-    const uint64_t below = (1ull << lane) - 1;
-
-    for (int e = lane; e <= a.experts; e += 64) place[wave][e] = 0;
-    __builtin_amdgcn_wave_barrier();
-    for (int64_t i = from; i < to; i += 64) {
-        const int e = expert_of(a, i + lane, to);
-        const uint64_t m = same_lanes(e, a.bits);
-        if (!(m & below)) place[wave][e] = place[wave][e] + __popcll(m);
-        __builtin_amdgcn_wave_barrier();
-    }
-    if (!ALONE) {
-        // the counts of all tiles, and of those before this one; threads share an expert's tiles
-        for (int e = tid; e < a.experts; e += kSortThreads) total[e] = before[e] = 0;
-        __syncthreads();
-        const int lanes = a.count_lanes, per = kSortThreads / lanes;
-        for (int e = tid % lanes; e < a.experts; e += lanes) {
-            int32_t all = 0, mine = 0;
-            for (int t = tid / lanes; t < a.tiles; t += per) {
-                const int32_t n = a.counts[(int64_t)t * a.experts + e];
-                all += n;
-                if (t < (int)blockIdx.x) mine += n;
-            }
-            atomicAdd(&total[e], all);
-            atomicAdd(&before[e], mine);
-        }
-    }
-    __syncthreads();
-    // thread t: experts 2 t and 2 t + 1; their totals, the waves' places within the group
-    uint32_t n[2] = {0, 0}, padded[2] = {0, 0};
+// Sums over the experts before, of n and padded: thread t has experts 2 t and 2 t + 1.
+struct Offsets {
+    uint32_t rows[2], scales[2], all_rows;
+};
+__device__ __forceinline__ Offsets offsets_of(const GroupArgs& a, const uint32_t (&n)[2],
+                                              uint32_t (*sums)[kSortWaves], bool store) {
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint32_t padded[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int e = 2 * tid + k;
-        if (e >= a.experts) continue;
-        int32_t run = ALONE ? 0 : before[e];
-#pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int32_t c = place[w][e];
-            place[w][e] = run;
-            run += c;
-        }
-        n[k] = (uint32_t)(ALONE ? run : total[e]);
-        padded[k] = (n[k] + a.pad - 1) / a.pad * a.pad;
-    }
-    // exclusive sums over the experts
+    for (int k = 0; k < 2; ++k) padded[k] = (n[k] + a.pad - 1) / a.pad * a.pad;
     uint32_t r = n[0] + n[1], s = padded[0] + padded[1];
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -362,51 +357,169 @@ __global__ void __launch_bounds__(kSortThreads) group_rows_kernel(const GroupArg
         sums[1][wave] = s;
     }
     __syncthreads();
-    uint32_t rows = 0;
+    Offsets o;
+    o.all_rows = 0;
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
         if (w < wave) {
             r += sums[0][w];
             s += sums[1][w];
         }
-        rows += sums[0][w];
+        o.all_rows += sums[0][w];
     }
     r -= n[0] + n[1];
     s -= padded[0] + padded[1];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int e = 2 * tid + k;
-        if (e < a.experts) {
-#pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) place[w][e] = place[w][e] + (int32_t)r;
-        }
-        if (e <= a.experts && blockIdx.x == 0) {
-            a.row_offsets[e] = r;
-            a.scales_offsets[e] = s;
+        o.rows[k] = r;
+        o.scales[k] = s;
+        if (store && 2 * tid + k <= a.experts) {
+            a.row_offsets[2 * tid + k] = r;
+            a.scales_offsets[2 * tid + k] = s;
         }
         r += n[k];
         s += padded[k];
     }
     // 1024 experts: the last offset is no thread's expert
-    if (blockIdx.x == 0 && tid == kSortThreads - 1 && a.experts == 2 * kSortThreads) {
+    if (store && tid == kSortThreads - 1 && a.experts == 2 * kSortThreads) {
         a.row_offsets[a.experts] = r;
         a.scales_offsets[a.experts] = s;
     }
+    return o;
+}
+
+// ALONE: all of the work.  Else the tile's ranks and counts.  KEEP: a wave has at most kKept steps.
+template <bool ALONE, bool KEEP>
+__global__ void __launch_bounds__(kSortThreads) group_rank_kernel(const GroupArgs a) {
+    // per wave and expert: its entries, then where its next one goes
+    __shared__ volatile int32_t place[kSortWaves][kMoeMaxExperts + 1];
+    __shared__ uint32_t sums[2][kSortWaves];
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t first = (int64_t)blockIdx.x * a.tile, tile_end = min(first + a.tile, a.entries);
+    const int64_t part = a.tile / kSortWaves;
+    const int64_t from = first + wave * part, to = min(from + part, tile_end);
+    const uint64_t below = (1ull << lane) - 1;
+
+    int e[kKept], rank[kKept];
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            e[k] = from + 64 * k < to ? expert_of(a, from + 64 * k + lane, to) : a.experts;
+    }
+    for (int x = lane; x <= a.experts; x += 64) place[wave][x] = 0;
+    __builtin_amdgcn_wave_barrier();
+    // one step: the entry's rank among the wave's of its expert so far
+    const auto step = [&](int x) {
+        const uint64_t m = same_lanes(x, a.bits);
+        const int r = place[wave][x] + __popcll(m & below);
+        __builtin_amdgcn_wave_barrier();
+        if (!(m & below)) place[wave][x] = r + __popcll(m);
+        __builtin_amdgcn_wave_barrier();
+        return r;
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (from + 64 * k < to) rank[k] = step(e[k]);
+    } else {
+        for (int64_t i = from; i < to; i += 64) step(expert_of(a, i + lane, to));
+    }
     __syncthreads();
-    for (int64_t i = from; i < to; i += 64) {
-        const int64_t at = i + lane;
-        const int e = expert_of(a, at, to);
-        const uint64_t m = same_lanes(e, a.bits);
-        const int32_t row = place[wave][e] + __popcll(m & below);
-        __builtin_amdgcn_wave_barrier();
-        if (!(m & below)) place[wave][e] = place[wave][e] + __popcll(m);
-        __builtin_amdgcn_wave_barrier();
-        if (at < to) {
-            if (e < a.experts) a.row_indices[row] = (int32_t)((uint32_t)at / (uint32_t)a.topk);
-            if (a.entry_rows) a.entry_rows[at] = e < a.experts ? row : -1;
+    // thread t: experts 2 t and 2 t + 1; their counts, the waves' places within the tile
+    uint32_t n[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int x = 2 * tid + k;
+        if (x >= a.experts) continue;
+        int32_t run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int32_t c = place[w][x];
+            place[w][x] = run;
+            run += c;
+        }
+        n[k] = (uint32_t)run;
+        if (!ALONE) a.counts[(int64_t)blockIdx.x * a.experts + x] = run;
+    }
+    uint32_t rows = 0;
+    if constexpr (ALONE) {
+        const Offsets o = offsets_of(a, n, sums, true);
+        rows = o.all_rows;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (2 * tid + k < a.experts) {
+#pragma unroll
+                for (int w = 0; w < kSortWaves; ++w)
+                    place[w][2 * tid + k] = place[w][2 * tid + k] + (int32_t)o.rows[k];
+            }
+    }
+    __syncthreads();
+    const auto put = [&](int64_t at, int x, int row) {
+        if (at >= to) return;
+        if constexpr (ALONE) {
+            if (x < a.experts) a.row_indices[row] = (int32_t)((uint32_t)at / (uint32_t)a.topk);
+            if (a.entry_rows) a.entry_rows[at] = x < a.experts ? row : -1;
+        } else {
+            a.ranks[at] = row;
+        }
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (from + 64 * k < to) put(from + 64 * k + lane, e[k], place[wave][e[k]] + rank[k]);
+    } else {
+        for (int64_t i = from; i < to; i += 64) {
+            const int x = expert_of(a, i + lane, to);
+            put(i + lane, x, step(x));
         }
     }
-    for (int64_t i = max(first, (int64_t)rows) + tid; i < tile_end; i += kSortThreads) a.row_indices[i] = -1;
+    if (ALONE)
+        for (int64_t i = (int64_t)rows + tid; i < tile_end; i += kSortThreads) a.row_indices[i] = -1;
+}
+
+// The tiles' entries to their rows.
+__global__ void __launch_bounds__(kSortThreads) group_place_kernel(const GroupArgs a) {
+    __shared__ int32_t total[kMoeMaxExperts], base[kMoeMaxExperts];
+    __shared__ uint32_t sums[2][kSortWaves];
+    const int tid = (int)threadIdx.x;
+    for (int x = tid; x < a.experts; x += kSortThreads) total[x] = base[x] = 0;
+    __syncthreads();
+    // the counts of all tiles, and of those before this one; threads share an expert's tiles
+    const int lanes = a.count_lanes, per = kSortThreads / lanes;
+    for (int x = tid % lanes; x < a.experts; x += lanes) {
+        int32_t all = 0, mine = 0;
+        for (int t0 = tid / lanes; t0 < a.tiles; t0 += 16 * per) {
+            int32_t c[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                c[k] = t0 + k * per < a.tiles ? a.counts[(int64_t)(t0 + k * per) * a.experts + x] : 0;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                all += c[k];
+                mine += t0 + k * per < (int)blockIdx.x ? c[k] : 0;
+            }
+        }
+        atomicAdd(&total[x], all);   // whole numbers: in any order
+        atomicAdd(&base[x], mine);
+    }
+    __syncthreads();
+    uint32_t n[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) n[k] = 2 * tid + k < a.experts ? (uint32_t)total[2 * tid + k] : 0u;
+    const Offsets o = offsets_of(a, n, sums, blockIdx.x == 0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (2 * tid + k < a.experts) base[2 * tid + k] += (int32_t)o.rows[k];
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.x * a.tile, end = min(first + a.tile, a.entries);
+    for (int64_t i = first + tid; i < end; i += kSortThreads) {
+        const int x = expert_of(a, i, end);
+        const int32_t row = x < a.experts ? base[x] + a.ranks[i] : -1;
+        if (row >= 0) a.row_indices[row] = (int32_t)((uint32_t)i / (uint32_t)a.topk);
+        if (a.entry_rows) a.entry_rows[i] = row;
+    }
+    for (int64_t i = max(first, (int64_t)o.all_rows) + tid; i < end; i += kSortThreads) a.row_indices[i] = -1;
 }
 
 // One workgroup takes so many entries.
@@ -444,13 +557,15 @@ void plan_group(GroupArgs& a) {
 }
 
 hipError_t launch_group(const GroupArgs& a, hipStream_t stream) {
+    const dim3 grid((uint32_t)a.tiles), block(kSortThreads);
+    const bool keep = a.tile <= kKept * kSortThreads;
     if (a.tiles == 1) {
-        hipLaunchKernelGGL((group_rows_kernel<true>), dim3(1), dim3(kSortThreads), 0, stream, a);
-    } else {
-        hipLaunchKernelGGL(group_count_kernel, dim3((uint32_t)a.tiles), dim3(kSortThreads), 0, stream, a);
-        hipLaunchKernelGGL((group_rows_kernel<false>), dim3((uint32_t)a.tiles), dim3(kSortThreads), 0,
-                           stream, a);
+        hipLaunchKernelGGL((group_rank_kernel<true, true>), grid, block, 0, stream, a);
+        return hipGetLastError();
     }
+    if (keep) hipLaunchKernelGGL((group_rank_kernel<false, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((group_rank_kernel<false, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL(group_place_kernel, grid, block, 0, stream, a);
     return hipGetLastError();
 }
 

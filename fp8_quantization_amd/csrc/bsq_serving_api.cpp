@@ -680,7 +680,7 @@ int64_t moe_group_rows_workspace(int64_t num_tokens, int64_t topk, int64_t num_e
     bsq::GroupArgs a{};
     if (check_group(num_tokens, topk, num_experts, &a) != BSQ_OK) return -1;
     ok();
-    return a.tiles == 1 ? 0 : (int64_t)a.tiles * num_experts * (int64_t)sizeof(int32_t);
+    return a.tiles == 1 ? 0 : (a.tiles * num_experts + a.entries) * (int64_t)sizeof(int32_t);
 }
 
 int moe_group_rows(const int32_t* topk_ids, int64_t num_tokens, int64_t topk, int64_t num_experts,
@@ -712,6 +712,7 @@ int moe_group_rows(const int32_t* topk_ids, int64_t num_tokens, int64_t topk, in
     a.row_indices = row_indices;
     a.entry_rows = entry_rows;
     a.counts = static_cast<int32_t*>(workspace);
+    if (need > 0) a.ranks = a.counts + a.tiles * num_experts;
     a.pad = (uint32_t)pad;
     return launched(bsq::launch_group(a, static_cast<hipStream_t>(stream)));
 }

@@ -187,7 +187,8 @@ struct GroupArgs {
     uint32_t* scales_offsets;
     int32_t* row_indices;
     int32_t* entry_rows;             // nullable
-    int32_t* counts;                 // [tiles][experts], workspace of more than one tile
+    int32_t* counts;                 // [tiles][experts], workspace of more than one tile,
+    int32_t* ranks;                  // and behind it [entries]: within the tile
     int32_t topk, experts;
     uint32_t pad;
     int64_t tile;                    // entries of a workgroup

@@ -188,7 +188,7 @@ def test_group_refusals(lib, kw):
 def test_group_workspace(lib):
     w = lib.moe_group_rows_workspace
     assert w(0, 1, 8) == 0 and w(64, 8, 256) == 0
-    assert w(16384, 8, 256) > 0 and w(16384, 8, 256) % (256 * 4) == 0
+    assert w(16384, 8, 256) > 4 * 16384 * 8 and w(16384, 8, 256) % (256 * 4) == 0
     assert w((1 << 31) - 1, 1, 1024) > 0
     assert w(-1, 1, 8) == -1 and w(1, 0, 8) == -1 and w(1, 1, 0) == -1 and lib.bsq_serving_last_error()
 
@@ -238,8 +238,8 @@ def test_logprobs_refusals(lib, kw, status):
 def test_logprobs_nothing_to_do_and_workspace(lib):
     assert logprobs(lib, R=0, z=None, tokens=None) == OK
     w = lib.token_logprobs_workspace
-    assert w(5, 2000, 4) == 0 and w(600, 8000, 4) == 0
-    assert w(1, 128000, 5) == 63 * (5 * 8 + 12) and w(2048, 128000, 20) == 2048 * 16 * (20 * 8 + 12)
+    assert w(5, 2000, 4) == 0 and w(3000, 8000, 4) == 0 and w(2048, 128000, 20) == 0
+    assert w(1, 128000, 5) == 63 * (5 * 8 + 12) and w(512, 128000, 20) == 512 * 4 * (20 * 8 + 12)
     assert w(1, 0, 0) == -1 and w(1, 5, 6) == -1 and w(1, 1 << 19, 1) == -1 and lib.bsq_serving_last_error()
 
 

@@ -262,3 +262,33 @@ def test_refusals_of_the_binding(bsq):  # noqa: F811
         args.update(kw)
         with pytest.raises(err):
             bsq.moe_group_rows(**args)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("step", [2.0 ** -25, 2.0 ** -22, 2.0 ** -19, 2.0 ** -16, 2.0 ** -13])
+@pytest.mark.parametrize("groups", [1, 8])
+def test_gaps_of_every_size(bsq, score, step, groups):  # noqa: F811
+    """Scores plus biases that lie `step` apart, or equal, in random order: sizes where 32 bits
+    tell them apart, where they cannot, and between."""
+    rng = np.random.default_rng(int(1 / step) % 1000 + groups)
+    E = 64
+    z = np.float32(rng.standard_normal((20, E)) * 1.5).astype(float)
+    s = 1 / (1 + np.exp(-z)) if score == "sigmoid" else np.exp(z) / np.exp(z).sum(1, keepdims=True)
+    for t in range(4):
+        place = rng.permutation(E) // (2 if t % 2 else 1)
+        b = np.float32(0.7 + place * step - s[t]).astype(float)
+        check(bsq, z[t:t + 1], 8, bias=b, score=score, groups=groups, keep=max(1, groups // 2), top=2)
+        # the same biases for other tokens: ordinary gaps beside
+        check(bsq, z, 8, bias=b, score=score, groups=groups, keep=max(1, groups // 2), top=1)
+
+
+def test_few_experts_left(bsq):  # noqa: F811
+    """As many experts with a finite choice as are asked for, one more and one less."""
+    rng = np.random.default_rng(0)
+    z = rng.standard_normal((3, 32))
+    for left in (3, 4, 5):
+        x = z.copy()
+        x[:, left:] = -np.inf
+        for score in ("softmax", "sigmoid"):
+            check(bsq, x, 4, bias=0.1 * rng.standard_normal(32), score=score)
+            check(bsq, x, 4, bias=0.1 * rng.standard_normal(32), score=score, groups=4, keep=2, top=2)
