@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
         const double pos = (double)a.positions[row] * 0.15915494309189533576888;   // 1 / (2 pi)
         float* all = reinterpret_cast<float*>(turns[threadIdx.x >> 6]);
         for (int i = lane; i < half; i += 64) sincos_turns(pos * a.inv_freq[i], all[i], all[128 + i]);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         if (turned) {
             const int i = PAIRS == kNeighbours ? d / 2 : low ? d : d - half;   // a multiple of 4

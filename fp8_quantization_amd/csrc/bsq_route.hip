@@ -112,6 +112,7 @@ __device__ __forceinline__ void close_groups(const RouteArgs& a, K (&key)[REGS],
 #pragma unroll
     for (int k = 0; k < REGS; ++k)
         if (64 * k + lane < a.experts) all[64 * k + lane] = c[k];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const int P = a.group_lanes, g = lane / P, first = g * a.group_size;
     F one = -INFINITY, two = -INFINITY;

@@ -44,9 +44,11 @@ def test_sizes(bsq, vocab, top, dtype):  # noqa: F811
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("rows,vocab", [(1, 130000), (600, 300), (513, 9001), (40, 131072), (2, 524280)])
+@pytest.mark.parametrize("rows,vocab", [(1, 130000), (600, 300), (513, 9001), (40, 131072), (2, 524280),
+                                        (900, 20011), (300, 50021)])
 def test_rows(bsq, rows, vocab, dtype):  # noqa: F811
-    """Short and long slices, with a join and without."""
+    """Short and long slices, of one chunk and of several, with a join and without; rows of odd
+    lengths, which begin anywhere in 16 bytes."""
     x, t = random(rows, vocab, dtype)
     check(bsq, x, t, 20)
 

@@ -183,6 +183,20 @@ def test_group_rows_of_uneven_choices(bsq, T):  # noqa: F811
 def test_group_rows_of_many_tiles(bsq):  # noqa: F811
     rng = np.random.default_rng(5)
     check_rows(bsq, (rng.random((60000, 5)) ** 3 * 200).astype(int), 200, 128)
+    # tiles of more entries than a wave keeps
+    ids = torch.tensor(rng.integers(-1, 1024, (70001, 9)), dtype=torch.int32, device="cuda")
+    rows, scales, index, entry = bsq.moe_group_rows(ids, 1024, pad=16)
+    flat = ids.view(-1).long()
+    key = torch.where(flat < 0, 1024, flat)
+    order = torch.sort(key, stable=True)[1]
+    counts = torch.bincount(key, minlength=1025)[:1024]
+    n = int(counts.sum())
+    assert torch.equal(rows[1:].long(), counts.cumsum(0)) and rows[0] == 0
+    assert torch.equal(scales[1:].long(), ((counts + 15) // 16 * 16).cumsum(0)) and scales[0] == 0
+    assert torch.equal(index[:n].long(), order[:n] // 9) and bool((index[n:] == -1).all())
+    back = torch.full_like(flat, -1)
+    back[order[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(entry.view(-1).long(), back)
     r = bsq.moe_group_rows(torch.empty((0, 3), dtype=torch.int32, device="cuda"), 70)
     torch.cuda.synchronize()
     assert not r[0].any() and not r[1].any() and r[0].numel() == 71 and r[2].numel() == 0
