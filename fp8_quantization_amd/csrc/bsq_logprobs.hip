@@ -24,6 +24,7 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256, kWaves = 4;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kMostFound = 2048;     // elements that are ranked at most
+constexpr int kFew = 256;            // and of a row's slices
 
 // A number and a place in the order of the answer: the larger number, then the lower place.
 // 0: nothing.
@@ -360,11 +361,45 @@ __global__ void __launch_bounds__(64) logprob_join_kernel(const LogprobArgs a) {
     l = wave_sum(l * f);
     t = wave_sum(t);
     finish<F32>(a, row, m, l, t);
-    // the best of the slices' next ones, again and again
+    if (a.top == 0) return;
     __syncthreads();
     const uint64_t* mine = lists + lane * a.top;
+    uint64_t head = on ? mine[0] : 0;
+    // As in a slice: the top-th of the lists' first entries (their numbers) is at most the top-th
+    // of all.  The entries that reach it are ranked by counting (the 20 best of 63 lists:
+    // 14.6 us a call, by the rounds below 17.4).
+    __shared__ uint64_t found[kFew];
+    __shared__ uint32_t count;
+    uint32_t bar = 0;
+#pragma unroll
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t with = bar | 1u << b;
+        if (__popcll(__ballot((uint32_t)(head >> 32) >= with)) >= a.top) bar = with;
+    }
+    if (bar > 0) {
+        if (lane == 0) count = 0;
+        __syncthreads();
+        for (int i = 0; on && i < a.top; ++i) {
+            const uint64_t e = mine[i];
+            if ((uint32_t)(e >> 32) < bar) break;
+            const uint32_t n = atomicAdd(&count, 1u);
+            if (n >= (uint32_t)kFew) break;
+            found[n] = e;
+        }
+        __syncthreads();
+        const int n = (int)count;
+        if (n <= kFew) {
+            for (int i = lane; i < n; i += 64) {
+                const uint64_t e = found[i];
+                int rank = 0;
+                for (int o = 0; o < n; ++o) rank += found[o] > e ? 1 : 0;
+                if (rank < a.top) store_top(a, row, rank, e, m, l);
+            }
+            return;
+        }
+    }
+    // fewer lists than that, or many equal numbers: the best of the next ones, again and again
     int next = 0;
-    uint64_t head = on && a.top > 0 ? mine[0] : 0;
     for (int r = 0; r < a.top; ++r) {
         const uint64_t e = wave_max(head);
         if (lane == 0) store_top(a, row, r, e, m, l);
@@ -384,8 +419,12 @@ void logprobs(const LogprobArgs& a, hipStream_t stream) {
                            (uint32_t)(a.slices * a.top * sizeof(uint64_t)), stream, a);
 }
 
+// Elements of a thread and chunk.  Short ones, one chunk a workgroup, where a row fits (2000 rows of
+// 1000: 8.5 us, long 11.6) or where long ones would leave few workgroups; else long ones, several
+// a workgroup as long as there are kWorkgroups (2048 rows of 128000: 105 us, with 4096 workgroups
+// 119, 8192 140).
+constexpr int kLong = 16, kShort = 8;
 constexpr int64_t kWorkgroups = 2048;
-constexpr int kLong = 16, kShort = 8;                // elements of a thread and chunk
 
 }  // namespace
 
@@ -394,7 +433,7 @@ void plan_logprobs(LogprobArgs& a) {
     const int64_t span = (int64_t)a.vocab + 7;
     const int64_t fine = (span + kThreads * kShort - 1) / (kThreads * kShort);
     const int64_t chunks = (span + kThreads * kLong - 1) / (kThreads * kLong);
-    if (fine <= 64 && a.rows * chunks < kWorkgroups / 4) {
+    if (fine == 1 || (fine <= 64 && a.rows * chunks < kWorkgroups / 4)) {
         a.slices = (int32_t)fine;
         a.per_thread = kShort;
         a.chunks = 1;

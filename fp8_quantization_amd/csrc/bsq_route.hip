@@ -524,9 +524,9 @@ __global__ void __launch_bounds__(kSortThreads) group_place_kernel(const GroupAr
 }
 
 // One workgroup takes so many entries.
-constexpr int64_t kAlone = 4096;
+constexpr int64_t kAlone = 2048;
 // Else tiles of this many at least, and at most that many tiles.
-constexpr int64_t kTile = 2048, kTiles = 128;
+constexpr int64_t kTile = 1024, kTiles = 128;
 
 }  // namespace
 
