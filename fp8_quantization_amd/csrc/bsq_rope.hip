@@ -9,9 +9,9 @@
 // sum over the L lanes; with halves a pair's other element is 8 elements of
 // another lane (rotary_dim being a multiple of 16), with neighbours it is the
 // lane's own.  Bound by the bytes: 16384 rows of 32 + 8 heads of 128 in BF16, 336
-// MB read and written, take 71 us (4.7 TB/s; a copy reaches 5.2).  With the
-// angles found by every lane for its own elements and lanes exchanged through
-// LDS it took 85.
+// MB read and written, take 75 us a call (4.5 TB/s; a copy reaches 5.2).  With
+// the angles found by every lane for its own elements and lanes exchanged
+// through LDS it took 85.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -19,7 +19,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 //
 // A wave a token, expert e in lane e % 64 of register e / 64.  The topk largest
 // are taken one after the other by the wave's largest key, a number's bits in
-// an order of unsigned integers (0: not to be chosen).
+// an order of unsigned integers (0: not to be chosen).  Bound by the chain of
+// these rounds for few tokens (64 of 256 experts in 8 groups, 8 chosen: 7.4 us a
+// call) and by their instructions for many: 16384 tokens of 128 experts take 9.2
+// us, some 280 vector instructions each, 16384 of 256 in 8 groups 28 (with
+// every score in 64 bits 33).
 
 // A logit; NaN counts as -inf.
 template <bool F32>
@@ -314,7 +318,9 @@ void route(const RouteArgs& a, bool f32, hipStream_t stream) {
 // number, so an entry's rank among them is a count of lanes, and no order of
 // atomics takes part.  Few entries are one workgroup's; of more, a first kernel
 // finds the ranks within the tiles and the tiles' counts, and a second adds up the
-// counts for each tile and places the entries.
+// counts for each tile and places the entries.  Bound by the latency of these
+// steps: 131072 entries of 256 experts take 13.4 us a call (with counts, then ranks
+// and places in one kernel 20.7), 512 take 7.0.
 
 constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
 constexpr int kKept = 8;             // steps of a wave whose entries stay in registers
@@ -523,9 +529,10 @@ __global__ void __launch_bounds__(kSortThreads) group_place_kernel(const GroupAr
     for (int64_t i = max(first, (int64_t)o.all_rows) + tid; i < end; i += kSortThreads) a.row_indices[i] = -1;
 }
 
-// One workgroup takes so many entries.
+// One workgroup takes so many entries (2048: 8.1 us; 4000 in one 11.4, in tiles 10.7).
 constexpr int64_t kAlone = 2048;
-// Else tiles of this many at least, and at most that many tiles.
+// Else tiles of this many at least, and at most that many tiles (32000 entries: 10.8 us, in tiles
+// of 2048 12.0, of 4096 16.4).
 constexpr int64_t kTile = 1024, kTiles = 128;
 
 }  // namespace
