@@ -614,13 +614,12 @@ __device__ __forceinline__ Places<MASKED> place_range(const AttendArgs& a, const
                                                       int ce, int& p0, int& p1) {
     Places<MASKED> r;
     page_range<MASKED>(a, sq, c0, ce, p0, p1);
-    if constexpr (MASKED) {
-        if (p1 > p0) {
-            r.sinks = min((int)(((int64_t)a.sinks + kKvPage - 1) / kKvPage), p0);
-            r.gap = p0 - r.sinks;
-            p1 -= r.gap;
-            p0 = 0;
-        }
+    if constexpr (MASKED) {          // the window may lie past the table, the sinks before its end
+        const int head = (int)(((int64_t)a.sinks + kKvPage - 1) / kKvPage);
+        r.sinks = min(min(head, p0), a.seqs.max_pages);
+        r.gap = p0 - r.sinks;
+        p1 -= r.gap;
+        p0 = 0;
     }
     return r;
 }
@@ -1123,7 +1122,27 @@ constexpr int64_t kRowsLeast = 4;
 // second holds 4 columns: 124 and 102).  A tree has many pairs to join, so the pages are split
 // only until there are kMaskedGroups workgroups (25 tokens over 20000, 56 workgroups: unsplit 67
 // us, in four 31, in twenty 31; 100 over 6000, 200 workgroups: 27, in two 37, in four 34).
+// Few columns of many pages are the form of many rows' again, its pages split: up to 80
+// workgroups of 128 columns from kManyPages on (48 tokens over 30000: 53 us, in blocks 76; 300
+// rows in 16000, 80 workgroups: 110 and 139; 100 over 10000, 157 pages: 42 and 42; 4 x 100 over
+// 10000, 128 workgroups: 104 and 82).  So are columns of head_dim 256, whose blocks are never two,
+// from 64 such workgroups on (1024 rows of 16 heads on 4 in a window of 4000, 128: 104 and 155;
+// 4 x 100 of 8 on 2, 32: 33 and 30).
 constexpr int64_t kMaskedRows = 512, kTwoBlocks = 768, kMaskedGroups = 256;
+constexpr int64_t kManyPages = 150;
+
+// The pages that one of a call's rows sees, or a block of them.
+int64_t pages_seen(int64_t max_kv, int64_t window, int64_t sinks, int64_t rows) {
+    const int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
+    if (window == 0 || window >= max_kv) return pages;
+    return std::min(pages, (window + rows) / kKvPage + 2 + (sinks + kKvPage - 1) / kKvPage);
+}
+
+bool masked_as_rows(double heads, int64_t head_dim, int64_t cols, int64_t pages) {
+    const double groups = heads * (double)((cols + kRowColumns - 1) / kRowColumns);
+    if (cols <= 64) return false;
+    return head_dim == 256 ? groups >= 64 || pages >= kManyPages : groups <= 80 && pages >= kManyPages;
+}
 
 AttendPlan plan_masked(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks, bool tree) {
@@ -1139,12 +1158,8 @@ AttendPlan plan_masked(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
         p.block_cols = 32;
     }
     p.col_blocks = (int32_t)((cols + p.block_cols - 1) / p.block_cols);
-    // the pages that a block's rows see
-    int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
-    if (window > 0 && window < max_kv) {
-        const int64_t rows = tree ? max_q : std::min(max_q, p.block_cols / group + 2);
-        pages = std::min(pages, (window + rows) / kKvPage + 2 + (sinks + kKvPage - 1) / kKvPage);
-    }
+    const int64_t pages = pages_seen(max_kv, window, sinks,
+                                     tree ? max_q : std::min(max_q, p.block_cols / group + 2));
     const double blocks = heads * p.col_blocks;
     int64_t run = std::max<int64_t>(pages, 1);
     if (!p.rows_form && pages > kSplitNone && blocks > 0) {
@@ -1161,7 +1176,10 @@ AttendPlan plan_masked(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
 
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks, bool tree) {
-    if ((tree || (sinks > 0 && window > 0)) && max_q * (num_q_heads / num_heads) > 16)
+    const bool masked = tree || (sinks > 0 && window > 0);
+    if (masked && max_q * (num_q_heads / num_heads) > 16 &&
+        !masked_as_rows((double)num_seqs * (double)num_heads, head_dim,
+                        max_q * (num_q_heads / num_heads), pages_seen(max_kv, window, sinks, 0)))
         return plan_masked(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks,
                            tree);
     const int64_t cols = max_q * (num_q_heads / num_heads);

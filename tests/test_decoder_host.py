@@ -110,6 +110,7 @@ def test_masked_workspace(lib):
     # trees: blocks of columns fill the chip, or their pages are split
     assert m(8, 128, 32, 16, 700, 48, 6000, 0, 0, 1) == 0
     assert m(8, 128, 32, 1, 25, 25, 20000, 0, 0, 1) > 0 and m(8, 128, 32, 1, 25, 25, 2000, 0, 0, 1) == 0
+    assert m(8, 128, 32, 1, 100, 100, 9000, 0, 0, 2) == 0 and m(8, 128, 32, 1, 100, 100, 10000, 0, 0, 2) > 0
 
 
 def test_reference_masks():

@@ -167,6 +167,20 @@ def test_forms_of_many_sequences(bsq, D, seqs, n, heads, hq):  # noqa: F811
     check(bsq, c, q, off, lens, table, D ** -0.5, 40, 4)
 
 
+@pytest.mark.parametrize("rows", [[1, 1], [9, 3], [100, 2]])
+@pytest.mark.parametrize("tree", [False, True])
+def test_tables_that_end_before_the_sequence(bsq, rows, tree):  # noqa: F811
+    """Tokens past the table's pages are not seen; the sinks are, also where the whole window is past
+    them."""
+    lens = [700, 300]
+    c, q, off, table = make(4, lens, rows, 2, 4, 64)
+    masks = trees(2, rows) if tree else None
+    for width in (1, 2, 4, 8):
+        cut = [r[:width] for r in table]
+        for window, sinks in ((90, 70), (90, 500), (400, 3), (90, 0)):
+            check(bsq, c, q, off, lens, cut, 0.125, window, sinks, masks)
+
+
 def test_rows_past_max_q_and_unowned_rows_are_left(bsq):  # noqa: F811
     rows, lens = [5, 9], [50, 70]
     c, q, off, table = make(1, lens, rows, 1, 2, 64)

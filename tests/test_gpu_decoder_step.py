@@ -214,6 +214,39 @@ def test_threads_on_their_own_streams(bsq):  # noqa: F811
     assert not errors and not any(t.is_alive() for t in threads)
 
 
+def test_outputs_that_c_callers_leave_out(bsq):  # noqa: F811
+    """NULL for v, entry_rows, entropy and the tokens, with the raw library: the other outputs stay."""
+    raw, g = bsq.serving_lib(), torch.Generator(device="cuda").manual_seed(1)
+    torch.cuda.synchronize()
+    for T in (30, 3000):
+        ids = torch.randint(0, 50, (T, 4), generator=g, device="cuda", dtype=torch.int32)
+        want = bsq.moe_group_rows(ids, 50, pad=16)
+        got = [torch.full_like(t, -9) for t in want[:3]]
+        ws = torch.empty(max(raw.moe_group_rows_workspace(T, 4, 50), 16), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert raw.moe_group_rows(ids.data_ptr(), T, 4, 50, 16, *(t.data_ptr() for t in got), None, ws.data_ptr(),
+                                  ws.numel(), None) == 0
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for V in (700, 30000):
+        z = torch.randn((3, V), generator=g, device="cuda")
+        want = bsq.token_logprobs(z, top=4)
+        ids, best = torch.full_like(want.top_ids, -9), torch.full_like(want.top_logprobs, -9)
+        ws = torch.empty(max(raw.token_logprobs_workspace(3, V, 4), 16), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert raw.token_logprobs(1, z.data_ptr(), V, 3, V, None, 0, 4, None, None, ids.data_ptr(), best.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(ids, want.top_ids) and torch.equal(best, want.top_logprobs)
+    x = torch.randn((5, 3, 64), generator=g, device="cuda")
+    q, k = torch.empty((2, 5, 64), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    assert raw.qk_norm_rope(1, x.data_ptr(), 192, 1, x.data_ptr() + 256, 192, 1, None, 0, 64, 5, None, None, 0.0, None,
+                            None, 0, 0, q.data_ptr(), 64, k.data_ptr(), 64, None, 0, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(q, x[:, 0].to(q.dtype)) and torch.equal(k, x[:, 1].to(k.dtype))
+
+
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
 @pytest.mark.parametrize("name", NAMES)
 def test_tensors_of_another_device(bsq, name):  # noqa: F811
