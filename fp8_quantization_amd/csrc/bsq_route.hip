@@ -21,9 +21,9 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // are taken one after the other by the wave's largest key, a number's bits in
 // an order of unsigned integers (0: not to be chosen).  Bound by the chain of
 // these rounds for few tokens (64 of 256 experts in 8 groups, 8 chosen: 7.4 us a
-// call) and by their instructions for many: 16384 tokens of 128 experts take 9.2
-// us, some 280 vector instructions each, 16384 of 256 in 8 groups 28 (with
-// every score in 64 bits 33).
+// call) and by their instructions for many: 16384 tokens of 256 experts in 8
+// groups take 28 us (with every score in 64 bits 33).  Where logits alone choose,
+// four tokens may share a wave.
 
 // A logit; NaN counts as -inf.
 template <bool F32>
@@ -303,6 +303,83 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) 
     }
 }
 
+// Four tokens a wave, for the choice by logits among all experts: expert 16 k + l is register k
+// of lane l of the token's 16.  A round's instructions serve four tokens, but look at four times the
+// registers one after the other.  In a graph, a wave a token against this:
+//   64 experts:   1 token 2.4 us, 2.4;     1024 tokens 2.9, 2.7;    16384 tokens 7.7, 3.9
+//   128 experts:  2048 tokens 3.4, 3.8;    4096 tokens 4.2, 3.8;    16384 tokens 9.0, 6.0
+//   256 experts:  4096 tokens 5.1, 5.7;    16384 tokens 11.3, 9.5
+template <int REGS, bool F32>
+__global__ void __launch_bounds__(kThreads) moe_route_many_kernel(const RouteArgs a) {
+    const int lane = (int)threadIdx.x & 63, l = lane & 15;
+    const int64_t token = ((int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6)) * 4 + (lane >> 4);
+    const bool on = token < a.tokens;
+    const auto largest = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+    const auto lowest = [](uint32_t x, uint32_t y) { return x < y ? x : y; };
+    const auto sum_of = [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) + __uint_as_float(y)); };
+    float x[REGS];
+    uint32_t key[REGS];
+#pragma unroll
+    for (int k = 0; k < REGS; ++k) {
+        const bool there = on && 16 * k + l < a.experts;
+        x[k] = there ? logit<F32>(a, token, 16 * k + l) : -INFINITY;
+        key[k] = there ? key_of(x[k]) : 0u;
+    }
+    uint32_t id = 0, mine = 0, top = 0;
+    for (int j = 0; j < a.topk; ++j) {
+        uint32_t best = key[0], at = 0;
+#pragma unroll
+        for (int k = 1; k < REGS; ++k) {
+            at = key[k] > best ? k : at;
+            best = max(best, key[k]);
+        }
+        const uint32_t most = row_all(best, largest);
+        const uint32_t e = row_all(best == most ? 16 * at + l : 0xFFFFu, lowest);
+        if (j == 0) top = most;
+        if (l == j) {
+            id = e;
+            mine = most;
+        }
+#pragma unroll
+        for (int k = 0; k < REGS; ++k) key[k] = e == 16u * k + l ? 0u : key[k];
+    }
+    // as weight_of
+    const float z = l < a.topk ? value_of(mine) : -INFINITY, t = value_of(top);
+    float s, sum;
+    if (a.sigmoid) {
+        const float m = a.renormalize && t < 0.0f && t > -INFINITY ? t : 0.0f;
+        s = (z > 0.0f ? 1.0f : share(z, m)) / (1.0f + __builtin_amdgcn_exp2f(-__builtin_fabsf(z) * kLog2e));
+        if (!(z > -INFINITY)) s = 0.0f;
+        sum = s;
+    } else {
+        s = sum = share(z, t);
+        if (!a.renormalize) {
+            sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < REGS; ++k) sum += share(x[k], t);
+        }
+    }
+    sum = __uint_as_float(row_all(__float_as_uint(sum), sum_of));
+    if (a.sigmoid && !a.renormalize) sum = 1.0f;
+    if (on && l < a.topk) {
+        a.ids[token * a.topk + l] = (int32_t)id;
+        a.weights[token * a.topk + l] = sum > 0.0f ? s / sum * a.factor : 0.0f;
+    }
+}
+
+// Whether four tokens share a wave: where that is not the slower one above.
+bool four_a_wave(const RouteArgs& a) {
+    if (a.bias || a.groups > 1 || a.experts > 256) return false;
+    return a.experts <= 64 || a.tokens >= (a.experts <= 128 ? 4096 : 8192);
+}
+
+template <int REGS>
+void route_many(const RouteArgs& a, bool f32, hipStream_t stream) {
+    const dim3 grid((uint32_t)((a.tokens + 4 * kWaves - 1) / (4 * kWaves)));
+    if (f32) hipLaunchKernelGGL((moe_route_many_kernel<REGS, true>), grid, dim3(kThreads), 0, stream, a);
+    else hipLaunchKernelGGL((moe_route_many_kernel<REGS, false>), grid, dim3(kThreads), 0, stream, a);
+}
+
 template <int REGS>
 void route(const RouteArgs& a, bool f32, hipStream_t stream) {
     const dim3 grid((uint32_t)((a.tokens + kWaves - 1) / kWaves));
@@ -545,6 +622,12 @@ void plan_route(RouteArgs& a) {
 }
 
 hipError_t launch_route(const RouteArgs& a, bool f32, hipStream_t stream) {
+    if (four_a_wave(a)) {
+        if (a.experts <= 64) route_many<4>(a, f32, stream);
+        else if (a.experts <= 128) route_many<8>(a, f32, stream);
+        else route_many<16>(a, f32, stream);
+        return hipGetLastError();
+    }
     if (a.experts <= 128) route<2>(a, f32, stream);
     else if (a.experts <= 256) route<4>(a, f32, stream);
     else route<kMoeMaxExperts / 64>(a, f32, stream);

@@ -24,14 +24,18 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t turned(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
-// f over the wave's numbers, in every lane: rotations by 8, 4, 2, 1 within the rows of 16 lanes,
-// then across them.
+// f over the numbers of a row of 16 lanes, in each of them: rotations by 8, 4, 2, 1.
 template <class F>
-__device__ __forceinline__ uint32_t wave_all(uint32_t v, F f) {
+__device__ __forceinline__ uint32_t row_all(uint32_t v, F f) {
     v = f(v, turned<0x128>(v));
     v = f(v, turned<0x124>(v));
     v = f(v, turned<0x122>(v));
-    v = f(v, turned<0x121>(v));
+    return f(v, turned<0x121>(v));
+}
+// f over the wave's numbers, in every lane.
+template <class F>
+__device__ __forceinline__ uint32_t wave_all(uint32_t v, F f) {
+    v = row_all(v, f);
     const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
     v = f(a[0], a[1]);
     const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);

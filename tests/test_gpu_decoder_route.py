@@ -132,6 +132,36 @@ def test_many_tokens(bsq):  # noqa: F811
     assert ids.shape == (0, 2) and w.shape == (0, 2)
 
 
+@pytest.mark.parametrize("E,k", [(5, 5), (16, 1), (17, 16), (64, 6), (65, 8), (128, 8), (129, 16), (200, 3), (256, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_four_tokens_a_wave(bsq, E, k, score, renorm):  # noqa: F811
+    """Many tokens without a bias: ties, masked experts and special logits among them."""
+    rng = np.random.default_rng(E + k)
+    z = rng.standard_normal((307 if E <= 64 else 4099 if E <= 128 else 8195, E)) * 2
+    z[:200] = np.round(z[:200])
+    z[200:220] *= 100
+    z[220:240] -= 300
+    z[240:260][rng.random((20, E)) < 0.7] = -np.inf
+    z[260:280][rng.random((20, E)) < 0.5] = np.nan
+    z[280:290][rng.random((10, E)) < 0.2] = np.inf
+    z[290], z[291] = -np.inf, np.nan
+    z[292, 0] = -0.0
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.tensor(z, device="cuda").to(dtype)
+        few = [bsq.moe_route(t, k, score=score, renormalize=renorm, factor=1.5) for t in x.split(2000)]
+        many = bsq.moe_route(x, k, score=score, renormalize=renorm, factor=1.5)
+        torch.cuda.synchronize()
+        assert torch.equal(many[0], torch.cat([f[0] for f in few]))
+        assert torch.allclose(many[1], torch.cat([f[1] for f in few]), rtol=2e-6, atol=1e-37)
+    check(bsq, z, k, score=score, renormalize=renorm, factor=1.5)
+    x = torch.tensor(z, device="cuda").to(torch.bfloat16)
+    wide = torch.full((len(z), E + 3), 1e9, device="cuda", dtype=torch.bfloat16)
+    wide[:, 1:E + 1] = x
+    for a, b in zip(bsq.moe_route(wide[:, 1:E + 1], k, score=score), bsq.moe_route(x, k, score=score)):
+        assert torch.equal(a, b)
+
+
 def test_route_agrees_with_moe_few_tokens(bsq):  # noqa: F811
     """Softmax routing chooses and weighs as moe_few_tokens does from the same logits."""
     from test_gpu_serving_moe import Layer
