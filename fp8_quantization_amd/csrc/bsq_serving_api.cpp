@@ -732,8 +732,8 @@ int token_logprobs(int dtype, const void* logits, int64_t ldl, int64_t num_rows,
     int st = check_dtype(dtype);
     if (st == BSQ_OK) st = check_logprobs(num_rows, vocab, top, &a);
     if (st != BSQ_OK) return st;
-    if (num_tokens < 0 || num_tokens > kMaxInt)
-        return fail(BSQ_ERR_INVALID_ARG, "num_tokens=%lld must be in 0 .. 2^31 - 1", (long long)num_tokens);
+    if (num_tokens < 0 || num_tokens > 1 << 30)   // a thread's index goes a workgroup past it
+        return fail(BSQ_ERR_INVALID_ARG, "num_tokens=%lld must be in 0 .. 2^30", (long long)num_tokens);
     if (num_rows == 0) return ok();
     if (!logits || (num_tokens > 0 && (!tokens || !logprobs)) || (top > 0 && (!top_ids || !top_logprobs)))
         return fail(BSQ_ERR_INVALID_ARG,

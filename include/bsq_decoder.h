@@ -175,7 +175,7 @@ int64_t moe_group_rows_workspace(int64_t num_tokens, int64_t topk, int64_t num_e
  *                   to the next, aligned to their size.
  *   vocab           1 .. 2^19 - 8 (more: BSQ_ERR_UNSUPPORTED).
  *   tokens          int32 [num_rows][num_tokens]; logprobs fp32, as tokens;
- *                   num_tokens 0 .. 2^31 - 1 (0: both may be NULL).
+ *                   num_tokens 0 .. 2^30 (0: both may be NULL).
  *   entropy         fp32 [num_rows], or NULL.
  *   top             0 .. 64, at most vocab.  top_ids, top_logprobs: int32 /
  *                   fp32 [num_rows][top].

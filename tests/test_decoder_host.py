@@ -236,6 +236,13 @@ def test_logprobs_refusals(lib, kw, status):
     assert lib.bsq_serving_last_error()
 
 
+def test_logprobs_tokens_of_a_row_at_most(lib):
+    """So many that a thread's index, 256 past the last, still is a number of 32 bits."""
+    assert logprobs(lib, R=0, n=1 << 30) == OK
+    for n in ((1 << 30) + 1, (1 << 31) - 1, 1 << 31):
+        assert logprobs(lib, R=0, n=n) == logprobs(lib, n=n) == INVALID
+
+
 def test_logprobs_nothing_to_do_and_workspace(lib):
     assert logprobs(lib, R=0, z=None, tokens=None) == OK
     w = lib.token_logprobs_workspace
