@@ -609,8 +609,12 @@ __global__ void __launch_bounds__(kSortThreads) group_place_kernel(const GroupAr
 // One workgroup takes so many entries (2048: 8.1 us; 4000 in one 11.4, in tiles 10.7).
 constexpr int64_t kAlone = 2048;
 // Else tiles of this many at least, and at most that many tiles (32000 entries: 10.8 us, in tiles
-// of 2048 12.0, of 4096 16.4).
-constexpr int64_t kTile = 1024, kTiles = 128;
+// of 2048 12.0, of 4096 16.4; 1048576 of 128 experts, in a graph: 22.8, in 128 tiles 36, in 512
+// 26.9).  Every workgroup reads the counts of all tiles and experts, so many experts take fewer:
+// tiles * experts counts are kCounts times a tile's entries at most (131072 entries of 1024
+// experts: 64 tiles 20.9, 128 26.9, 32 22.0).
+constexpr int64_t kTile = 1024, kTiles = 256;
+constexpr double kCounts = 32.0;
 
 }  // namespace
 
@@ -638,7 +642,9 @@ void plan_group(GroupArgs& a) {
     a.bits = 0;
     while ((1 << a.bits) <= a.experts) ++a.bits;
     a.tiles = 1;
-    if (a.entries > kAlone) a.tiles = (int32_t)std::min(kTiles, (a.entries + kTile - 1) / kTile);
+    if (a.entries > kAlone)
+        a.tiles = (int32_t)std::min({kTiles, (a.entries + kTile - 1) / kTile,
+                                     (int64_t)sqrt(kCounts * (double)a.entries / a.experts)});
     const int64_t per = (a.entries + a.tiles - 1) / a.tiles;
     a.tile = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
     a.tiles = a.tile > 0 ? (int32_t)((a.entries + a.tile - 1) / a.tile) : 1;

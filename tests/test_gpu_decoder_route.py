@@ -232,6 +232,12 @@ def test_group_rows_of_many_tiles(bsq):  # noqa: F811
     assert not r[0].any() and not r[1].any() and r[0].numel() == 71 and r[2].numel() == 0
 
 
+@pytest.mark.parametrize("E", [3, 130])
+def test_group_rows_of_the_most_tiles(bsq, E):  # noqa: F811
+    rng = np.random.default_rng(E)
+    check_rows(bsq, rng.integers(-1, E + 1, (300001, 4)), E, 16)
+
+
 def test_group_rows_outputs_of_the_callers(bsq):  # noqa: F811
     ids = np.random.default_rng(6).integers(0, 8, (900, 6))
     want = check_rows(bsq, ids, 8, 16)
