@@ -1049,7 +1049,7 @@ void attend_rows(const AttendArgs& a, dim3 grid, hipStream_t stream) {
 }
 
 template <int D, bool MASKED>
-void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+hipError_t attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
     const int64_t per = (int64_t)a.seqs.num_seqs * a.cache.num_heads * a.col_blocks;
     const dim3 grid((uint32_t)(per * a.splits));
     if (p.rows_form) {
@@ -1063,6 +1063,8 @@ void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
                 hipLaunchKernelGGL((attend_split_kernel<D, 2, 8, false, true>), grid, dim3(512), 0, stream, a);
             else
                 hipLaunchKernelGGL((attend_split_kernel<D, 2, 4, false, true>), grid, dim3(256), 0, stream, a);
+        } else {
+            return hipErrorInvalidConfiguration;   // no plan of these kernels
         }
     } else if (p.wide) {
         hipLaunchKernelGGL((attend_split_kernel<D, 1, 8, false, MASKED>), grid, dim3(512), 0, stream, a);
@@ -1081,6 +1083,7 @@ void attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
             hipLaunchKernelGGL((attend_join_kernel<D, kWaves, MASKED>), dim3((uint32_t)pairs),
                                dim3(kThreads), 0, stream, a);
     }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -1149,6 +1152,7 @@ AttendPlan plan_masked(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
     const int64_t group = num_q_heads / num_heads, cols = max_q * group;
     const double heads = (double)num_seqs * (double)num_heads;
     AttendPlan p{};
+    p.masked = true;
     p.rows_form = cols > 64 && heads * (double)cols >= (double)kMaskedRows * kRowColumns;
     p.block_cols = 16;
     if (p.rows_form) {
@@ -1184,6 +1188,7 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
                            tree);
     const int64_t cols = max_q * (num_q_heads / num_heads);
     AttendPlan p{};
+    p.masked = masked;
     p.rows_form = cols > 64;
     int64_t pages = (max_kv + kKvPage - 1) / kKvPage;
     if (window > 0 && window < max_kv) {
@@ -1229,19 +1234,17 @@ AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
 
 namespace {
 template <bool MASKED>
-void attend_of(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+hipError_t attend_of(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
     switch (a.cache.head_dim) {
-        case 64: attend<64, MASKED>(a, p, stream); break;
-        case 128: attend<128, MASKED>(a, p, stream); break;
-        default: attend<256, MASKED>(a, p, stream); break;
+        case 64: return attend<64, MASKED>(a, p, stream);
+        case 128: return attend<128, MASKED>(a, p, stream);
+        default: return attend<256, MASKED>(a, p, stream);
     }
 }
 }  // namespace
 
 hipError_t launch_kv_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
-    if (a.masks || (a.sinks > 0 && a.window > 0)) attend_of<true>(a, p, stream);
-    else attend_of<false>(a, p, stream);
-    return hipGetLastError();
+    return p.masked ? attend_of<true>(a, p, stream) : attend_of<false>(a, p, stream);
 }
 
 }  // namespace bsq

@@ -126,6 +126,9 @@ int check_seqs(const uint32_t* row_offsets, const int32_t* kv_lens, const int32_
     return BSQ_OK;
 }
 
+// A call's window: one longer than any sequence is none, for the plan as for the kernels.
+int64_t window_of(int64_t window) { return window > kMaxInt ? 0 : window; }
+
 // The query heads and sizes of an attention call, and how its work is cut.
 int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs, int64_t max_q,
          int64_t max_kv, int64_t window, int64_t sinks, bool tree, bsq::AttendPlan* p) {
@@ -149,8 +152,8 @@ int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_s
         *p = bsq::AttendPlan{};
         return BSQ_OK;
     }
-    *p = bsq::plan_attend(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks,
-                          tree);
+    *p = bsq::plan_attend(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv,
+                          window_of(window), sinks, tree);
     const double blocks = (double)num_seqs * (double)num_heads * (double)p->col_blocks * p->splits;
     const double pairs = (double)num_seqs * (double)max_q * (double)num_q_heads;
     // the join has at least a wave for each pair
@@ -341,7 +344,7 @@ int kv_cache_attention_masked(const bsq_kv_cache* cache, const void* q, int64_t 
     a.part_o = static_cast<float*>(workspace);
     if (need > 0)
         a.part_ml = a.part_o + (int64_t)p.splits * num_rows * num_q_heads * cache->head_dim;
-    a.window = window > kMaxInt ? 0 : window;      // longer than any sequence; its places stay in 64 bits
+    a.window = window_of(window);
     a.masks = masks;
     a.mask_words = masks ? (int32_t)mask_words : 0;
     a.sinks = (int32_t)sinks;

@@ -77,6 +77,7 @@ struct AttendPlan {
     int32_t split_pages;
     bool wide;                       // eight waves a workgroup instead of four (both forms)
     int32_t threads;                 // of a workgroup
+    bool masked;                     // the kernels that know trees and sinks
 };
 AttendPlan plan_attend(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_seqs,
                        int64_t max_q, int64_t max_kv, int64_t window, int64_t sinks, bool tree);

@@ -113,6 +113,16 @@ def test_masked_workspace(lib):
     assert m(8, 128, 32, 1, 100, 100, 9000, 0, 0, 2) == 0 and m(8, 128, 32, 1, 100, 100, 10000, 0, 0, 2) > 0
 
 
+@pytest.mark.parametrize("sizes", [(8, 128, 32, 1, 25, 25, 20000), (8, 128, 32, 1, 100, 100, 10000),
+                                   (2, 64, 8, 2, 60, 30, 9000), (8, 256, 32, 1, 40, 40, 30000)])
+def test_masked_workspace_of_windows_longer_than_any_sequence(lib, sizes):
+    """A window past 2^31 - 1 is none, beside sinks too."""
+    m = lib.kv_cache_attention_masked_workspace
+    for window in (1 << 31, 1 << 40, (1 << 63) - 1):
+        for words in (0, 2):
+            assert m(*sizes, window, 4, words) == m(*sizes, 0, 4, words)
+
+
 def test_reference_masks():
     """The reference's masks by hand: 5 rows after 4 tokens."""
     def see(*a):

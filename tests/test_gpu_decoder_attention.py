@@ -167,6 +167,24 @@ def test_forms_of_many_sequences(bsq, D, seqs, n, heads, hq):  # noqa: F811
     check(bsq, c, q, off, lens, table, D ** -0.5, 40, 4)
 
 
+@pytest.mark.parametrize("window", [1 << 31, (1 << 31) + 64, 1 << 40, (1 << 63) - 1])
+@pytest.mark.parametrize("D,seqs,n,heads,hq", [
+    (128, 64, 8, 8, 32), (128, 64, 5, 8, 32), (128, 16, 48, 8, 32), (64, 65, 9, 4, 16),   # blocks of 32 columns
+    (256, 30, 9, 8, 32), (128, 2, 9, 2, 8), (64, 2, 1, 2, 8), (128, 2, 100, 2, 8)])
+def test_windows_longer_than_any_sequence(bsq, D, seqs, n, heads, hq, window):  # noqa: F811
+    """A window past 2^31 - 1 is none: every token is seen, the sinks among them, and the call is
+    kv_cache_attention's, bit for bit."""
+    rows, lens = [n] * seqs, [n + 7 * (s * 13 % 17) for s in range(seqs)]
+    c, q, off, table = make(2, lens, rows, heads, hq, D)
+    d = dev_cache(bsq, c)
+    want = bsq.kv_cache_attention(dev_rows(q), d, i32(off), i32(lens), i32(table), n, max(lens), scale=0.1,
+                                  return_lse=True)
+    out, lse = torch.full_like(want[0], 5.0), torch.full_like(want[1], 5.0)
+    call(bsq, c, q, off, lens, table, 0.1, window, 4, dev=d, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("rows", [[1, 1], [9, 3], [100, 2]])
 @pytest.mark.parametrize("tree", [False, True])
 def test_tables_that_end_before_the_sequence(bsq, rows, tree):  # noqa: F811
