@@ -167,6 +167,42 @@ def test_forms_of_many_sequences(bsq, D, seqs, n, heads, hq):  # noqa: F811
     check(bsq, c, q, off, lens, table, D ** -0.5, 40, 4)
 
 
+@pytest.mark.parametrize("D,heads,hq", [(128, 8, 32), (64, 8, 32)])
+@pytest.mark.parametrize("seqs,n", [(64, 6), (48, 8), (32, 16)])
+def test_batches_of_small_trees(bsq, D, heads, hq, seqs, n):  # noqa: F811
+    """Blocks of 32 columns whose pages eight waves share; lengths in random order, some of one page
+    or without tokens before the tree."""
+    rows = [n - s % 3 for s in range(seqs)]
+    lens = [r + (s * 37 % 23) * 13 for s, r in enumerate(rows)]
+    c, q, off, table = make(5, lens, rows, heads, hq, D)
+    check(bsq, c, q, off, lens, table, D ** -0.5, 0, 0, trees(4, rows))
+    check(bsq, c, q, off, lens, table, D ** -0.5, 90, 5, trees(4, rows))
+    check(bsq, c, q, off, lens, table, D ** -0.5, 40, 70)
+
+
+@pytest.mark.parametrize("D,seqs,n,heads,hq", [(128, 65, 1, 8, 32), (64, 70, 1, 8, 16), (256, 80, 1, 8, 16),
+                                               (128, 33, 2, 16, 64), (64, 33, 3, 16, 64)])
+@pytest.mark.parametrize("longest", [300, 3300])
+def test_batches_of_few_columns(bsq, D, seqs, n, heads, hq, longest):  # noqa: F811
+    """One block of 16 columns a sequence and more workgroups than CUs: pages read past the caches,
+    unsplit and in runs that a wave for each pair joins."""
+    rows = [n] * seqs
+    lens = [longest if s == 5 else n + (s * 29 % 31) * 11 for s in range(seqs)]
+    c, q, off, table = make(6, lens, rows, heads, hq, D)
+    check(bsq, c, q, off, lens, table, D ** -0.5, longest - 200, 70)
+    check(bsq, c, q, off, lens, table, D ** -0.5, 100, 4)
+    check(bsq, c, q, off, lens, table, D ** -0.5, 0, 0, trees(7, rows))
+
+
+@pytest.mark.parametrize("D,n,heads,hq", [(64, 100, 2, 4), (64, 40, 2, 4), (256, 100, 2, 4)])
+def test_few_columns_of_many_pages(bsq, D, n, heads, hq):  # noqa: F811
+    """The form of many rows, its pages in runs of several workgroups."""
+    rows, lens = [n, 3], [9990, 70]
+    c, q, off, table = make(8, lens, rows, heads, hq, D)
+    check(bsq, c, q, off, lens, table, D ** -0.5, 0, 0, trees(9, rows))
+    check(bsq, c, q, off, lens, table, D ** -0.5, 9700, 70)
+
+
 @pytest.mark.parametrize("window", [1 << 31, (1 << 31) + 64, 1 << 40, (1 << 63) - 1])
 @pytest.mark.parametrize("D,seqs,n,heads,hq", [
     (128, 64, 8, 8, 32), (128, 64, 5, 8, 32), (128, 16, 48, 8, 32), (64, 65, 9, 4, 16),   # blocks of 32 columns
