@@ -174,12 +174,16 @@ __device__ __forceinline__ float weight_of(const RouteArgs& a, float z, const fl
             for (int k = 1; k < REGS; ++k) top = fmaxf(top, x[k]);
         }
         top = wave_max(top);
-        s = share(z, top);
-        sum = s;
+        s = sum = share(z, top);
         if (!a.renormalize) {
             sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < REGS; ++k) sum += share(x[k], top);
+        } else {                     // an infinite one that is not chosen leaves the chosen nothing
+            bool infinite = false;
+#pragma unroll
+            for (int k = 0; k < REGS; ++k) infinite |= x[k] == INFINITY;
+            if (top < INFINITY && __any(infinite)) sum = 0.0f;
         }
         sum = wave_sum(sum);
     }

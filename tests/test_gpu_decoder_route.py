@@ -109,6 +109,44 @@ def test_special_logits(bsq, score, renorm, bias):  # noqa: F811
         check(bsq, z, 4, bias=b, score=score, renormalize=renorm, **g)
 
 
+@pytest.mark.parametrize("E", [16, 200, 400])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_infinite_logits_that_are_not_chosen(bsq, E, renorm, dtype):  # noqa: F811
+    """Under softmax they take the whole score all the same: where the chosen experts have none of
+    it, their weights are 0."""
+    inf, nan = np.inf, np.nan
+    rng = np.random.default_rng(E)
+    z, b = rng.standard_normal((6, E)), 0.1 * rng.standard_normal(E)
+    b[[1, 5, 9]] = -inf, nan, -3.0
+    z[0, 1] = z[1, 5] = z[2, 9] = inf
+    z[3, [1, 5, 9]] = inf
+    z[4, [1, 7]] = inf               # one of two is chosen
+    x = torch.tensor(z, device="cuda").to(dtype)
+    z, bf = x.double().cpu().numpy(), torch.tensor(b).float().double().numpy()
+    for kw in (dict(), dict(groups=4, keep=3), dict(groups=4, keep=3, top=2)):
+        want = R.route(z, 4, "softmax", bias=bf, renormalize=renorm, factor=1.5, **kw)
+        s = np.isinf(z) / np.maximum(np.isinf(z).sum(1, keepdims=True), 1)
+        s = np.take_along_axis(s, want[0], 1)[:5]
+        total = s.sum(1, keepdims=True) if renorm else 1.0
+        ids, w = bsq.moe_route(x, 4, bias=torch.tensor(b, device="cuda").float(), renormalize=renorm, factor=1.5,
+                               **{dict(groups="num_groups", keep="topk_groups", top="group_top")[k]: v
+                                  for k, v in kw.items()})
+        torch.cuda.synchronize()
+        assert np.array_equal(ids.cpu().numpy(), want[0])
+        got = w.double().cpu().numpy()
+        assert np.array_equal(got[:5], np.where(total > 0, 1.5 * s / np.maximum(total, 1e-9), 0.0))
+        assert not got[:4].any() and got[4].any() and np.all(np.abs(got[5] - want[1][5]) <= want[2][5])
+    # no bias: a group whose second best is -inf is not kept
+    z = np.full((1, E), 0.5)
+    z[0, :E // 4] = -inf
+    z[0, 3] = inf
+    ids, w = bsq.moe_route(torch.tensor(z, device="cuda").to(dtype), 4, num_groups=4, topk_groups=2, group_top=2,
+                           renormalize=renorm)
+    torch.cuda.synchronize()
+    assert ids[0].tolist() == [E // 4 + i for i in range(4)] and not w.any()
+
+
 def test_rows_of_a_larger_tensor(bsq):  # noqa: F811
     """A row stride, an odd offset of BF16 elements, outputs of the caller's."""
     rng = np.random.default_rng(2)
