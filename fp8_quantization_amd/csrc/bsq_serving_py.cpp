@@ -644,7 +644,9 @@ PyObject* route(Args& a) {
     const at::Tensor* weights = a.tensor("topk_weights", true);
     const CallStream stream(a);
     const int64_t T = logits.size(0), E = logits.size(1);
-    if (k < 1) refuse(BSQ_ERR_INVALID_ARG, "topk=%lld must be at least 1", (long long)k);
+    // before memory for the outputs is taken
+    if (k < 1 || k > E)
+        refuse(BSQ_ERR_INVALID_ARG, "topk=%lld must be in 1 .. the %lld experts", (long long)k, (long long)E);
     if (top < 1 || top > 2) refuse(BSQ_ERR_INVALID_ARG, "group_top=%lld must be 1 or 2", (long long)top);
     if (bias) vec(bias, "bias", at::kFloat, E, true);
     at::Tensor new_ids, new_weights;

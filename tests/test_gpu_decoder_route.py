@@ -352,6 +352,14 @@ def test_refusals_of_the_binding(bsq):  # noqa: F811
             bsq.moe_group_rows(**args)
 
 
+@pytest.mark.parametrize("topk", [17, 1025, 1 << 31, 1 << 40, (1 << 63) - 1])
+@pytest.mark.parametrize("T", [0, 4])
+def test_far_topk_is_refused_before_memory_is_taken(bsq, topk, T):  # noqa: F811
+    z = torch.zeros((T, 16), device="cuda")
+    with pytest.raises(bsq.BsqError, match="topk"):
+        bsq.moe_route(z, topk)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("step", [2.0 ** -25, 2.0 ** -22, 2.0 ** -19, 2.0 ** -16, 2.0 ** -13])
 @pytest.mark.parametrize("groups", [1, 8])
