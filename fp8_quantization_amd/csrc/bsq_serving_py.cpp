@@ -518,7 +518,9 @@ PyObject* moe(Args& a) {
     if (H % 128 != 0 || I % 128 != 0)
         refuse(BSQ_ERR_INVALID_ARG, "hidden=%lld and inter=%lld must be multiples of 128",
                (long long)H, (long long)I);
-    if (k < 1) refuse(BSQ_ERR_INVALID_ARG, "topk=%lld must be at least 1", (long long)k);
+    // before memory for the outputs is taken
+    if (k < 1 || k > E)
+        refuse(BSQ_ERR_INVALID_ARG, "topk=%lld must be in 1 .. the %lld experts", (long long)k, (long long)E);
     auto width = [&](int64_t K) { return fmt == BSQ_MXFP8 ? K : K / 2; };
     auto records = [](int64_t K) { return (K + 511) / 512 * 256; };
     matrix(w13, "w13_codes", at::kByte, 2 * E * I, width(H));

@@ -248,3 +248,11 @@ def test_no_tokens_and_refusals(bsq):  # noqa: F811
         with pytest.raises(bad):
             bsq.moe_few_tokens(a["x"], a["fmt"], *w, a["E"], a["k"], router_logits=a["router_logits"],
                                out=a["out"])
+
+
+@pytest.mark.parametrize("topk", [13, 1 << 31, 1 << 40, (1 << 63) - 1])
+def test_far_topk_is_refused_before_memory_is_taken(bsq, topk):  # noqa: F811
+    L = Layer(3, 12, 256, 128, "mxfp4")
+    x, z = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda"), torch.zeros((4, 12), device="cuda")
+    with pytest.raises(bsq.BsqError, match="topk"):
+        bsq.moe_few_tokens(x, "mxfp4", *L.dev(), 12, topk, router_logits=z)
