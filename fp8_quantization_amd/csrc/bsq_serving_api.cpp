@@ -162,6 +162,14 @@ int plan(int64_t num_heads, int64_t head_dim, int64_t num_q_heads, int64_t num_s
     return BSQ_OK;
 }
 
+// The words of a row's mask.
+int check_masks(int64_t mask_words, int64_t max_q) {
+    if (mask_words < 0 || mask_words > kMaxInt || 64 * mask_words < max_q)
+        return fail(BSQ_ERR_INVALID_ARG, "mask_words=%lld must hold max_q=%lld bits",
+                    (long long)mask_words, (long long)max_q);
+    return BSQ_OK;
+}
+
 int64_t attend_workspace(const bsq::AttendPlan& p, int64_t num_rows, int64_t num_q_heads,
                          int64_t head_dim) {
     if (p.splits <= 1) return 0;
@@ -277,12 +285,12 @@ int64_t kv_cache_attention_masked_workspace(int64_t num_heads, int64_t head_dim,
                                             int64_t num_rows, int64_t max_q, int64_t max_kv,
                                             int64_t window, int64_t sinks, int64_t mask_words) {
     bsq::AttendPlan p;
-    if (num_rows < 0 || num_rows > kMaxInt || sinks < 0 || sinks > kMaxInt || mask_words < 0) {
-        fail(BSQ_ERR_INVALID_ARG,
-             "num_rows=%lld and sinks=%lld must be in 0 .. 2^31 - 1, mask_words=%lld >= 0",
-             (long long)num_rows, (long long)sinks, (long long)mask_words);
+    if (num_rows < 0 || num_rows > kMaxInt || sinks < 0 || sinks > kMaxInt) {
+        fail(BSQ_ERR_INVALID_ARG, "num_rows=%lld and sinks=%lld must be in 0 .. 2^31 - 1",
+             (long long)num_rows, (long long)sinks);
         return -1;
     }
+    if (mask_words != 0 && check_masks(mask_words, max_q) != BSQ_OK) return -1;
     if (plan(num_heads, head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks, mask_words > 0,
              &p) != BSQ_OK)
         return -1;
@@ -319,9 +327,7 @@ int kv_cache_attention_masked(const bsq_kv_cache* cache, const void* q, int64_t 
     if (st != BSQ_OK) return st;
     if (sinks < 0 || sinks > kMaxInt)
         return fail(BSQ_ERR_INVALID_ARG, "sinks=%lld must be in 0 .. 2^31 - 1", (long long)sinks);
-    if (masks && (mask_words < 0 || mask_words > kMaxInt || 64 * mask_words < max_q))
-        return fail(BSQ_ERR_INVALID_ARG, "mask_words=%lld must hold max_q=%lld bits",
-                    (long long)mask_words, (long long)max_q);
+    if (masks && (st = check_masks(mask_words, max_q)) != BSQ_OK) return st;
     if (masks && !aligned(masks, 8)) return fail(BSQ_ERR_INVALID_ARG, "masks must be 8-byte aligned");
     st = plan(cache->num_heads, cache->head_dim, num_q_heads, num_seqs, max_q, max_kv, window, sinks,
               masks != nullptr, &p);

@@ -113,6 +113,16 @@ def test_masked_workspace(lib):
     assert m(8, 128, 32, 1, 100, 100, 9000, 0, 0, 2) == 0 and m(8, 128, 32, 1, 100, 100, 10000, 0, 0, 2) > 0
 
 
+def test_masked_workspace_of_masks_that_the_call_refuses(lib):
+    """Words that do not hold max_q bits, or are too many."""
+    m = lib.kv_cache_attention_masked_workspace
+    for max_q, words in ((65, 1), (129, 2), (20000, 300), (1, 1 << 31), (1, 1 << 62)):
+        assert masked(lib, max_q=max_q, words=words) == INVALID
+        assert m(2, 128, 4, 2, 8, max_q, 20000, 0, 0, words) == -1 and lib.bsq_serving_last_error()
+    for max_q, words in ((64, 1), (65, 2), (128, 2), (0, 1)):
+        assert m(2, 128, 4, 2, 8, max_q, 20000, 0, 0, words) >= 0
+
+
 @pytest.mark.parametrize("sizes", [(8, 128, 32, 1, 25, 25, 20000), (8, 128, 32, 1, 100, 100, 10000),
                                    (2, 64, 8, 2, 60, 30, 9000), (8, 256, 32, 1, 40, 40, 30000)])
 def test_masked_workspace_of_windows_longer_than_any_sequence(lib, sizes):
