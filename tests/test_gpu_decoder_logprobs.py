@@ -226,3 +226,46 @@ def test_ties_of_many_in_long_slices(bsq, vocab):  # noqa: F811
     assert np.array_equal(got.top_ids[:5].cpu().numpy(), ids)
     assert np.all(np.abs(got.top_logprobs[:5].double().cpu().numpy() - best) <= bb)
     assert bool((got.top_ids[5:] == torch.arange(16, device="cuda")).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(2048, 100003), (600, 131072)])
+def test_many_rows_of_many_chunks(bsq, rows, vocab, dtype):  # noqa: F811
+    """Slices of 7 and of 25 chunks: hundreds of terms a thread, random ones, rising ones, whose sums
+    are rescaled at every chunk, and equal ones.
+
+    Bounds, U = 2^-24.  A term is off by 4 (|d| + 2) U of it, d = z - max (its exponent's rounding,
+    the hardware's exponential, and the same again where slices meet).  A thread adds 16 terms for each
+    of up to C = (vocab + 7) / 4096 chunks, all of one sign: 16 C U of the sum.  A rescale costs 3 U and
+    the rounding of its exponent, at most C + 2 times (the threads' and the slices' meeting among them):
+    3 (C + 2) U, and U for each unit of e that the largest rises, at most the row's range.  Six and three
+    sums over the threads and six over slices: 15 U.  All of that holds for the sum of s and for that of
+    s d.  The base-2 logarithm is off by 2 U of it and U; a product and a difference follow."""
+    U = 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = (torch.randn((rows, vocab), generator=g, device="cuda") * 2.5).to(dtype)
+    x[1] = torch.linspace(-9, 9, vocab, device="cuda").to(dtype)
+    x[2] = torch.linspace(-60, 20, vocab, device="cuda").to(dtype)
+    x[3] = -7.25
+    some = [0, 1, 2, 3, rows // 2, rows - 1]
+    t = torch.randint(0, vocab, (rows, 4), generator=g, device="cuda", dtype=torch.int32)
+    got = bsq.token_logprobs(x, t, top=20)
+    torch.cuda.synchronize()
+    z, t = x[some].double().cpu().numpy(), t[some].cpu().numpy()
+    lp, H, ids, best, *_ = R.logprobs(z, t, 20)
+    assert np.array_equal(got.top_ids[some].cpu().numpy(), ids)
+    C = (vocab + 7 + 4095) // 4096
+    for r in range(len(some)):
+        d = z[r] - z[r].max()
+        p = np.exp(d)
+        log_l = np.log(p.sum())
+        p /= p.sum()
+        sums = (16 * C + 3 * (C + 2) + 15 - d.min()) * U
+        off = (p * (np.abs(d) + 2)).sum() * 4 * U + sums
+        off_log = off * (1 + 2.0 ** -10) + 6 * U * log_l + 2 * U
+        for a, want, at in ((got.logprobs, lp, t[r]), (got.top_logprobs, best, ids[r])):
+            bound = off_log + (np.abs(d[at]) + np.abs(want[r])) * 2 * U
+            assert np.all(np.abs(a[some[r]].double().cpu().numpy() - want[r]) <= bound), r
+        bound = off_log + (p * np.abs(d)).sum() * (off + sums + 8 * U) + \
+            (p * np.abs(d) * (np.abs(d) + 2)).sum() * 4 * U + 4 * U * (H[r] + log_l)
+        assert abs(got.entropy[some[r]].item() - H[r]) <= bound, r
