@@ -109,6 +109,31 @@ def test_special_logits(bsq, score, renorm, bias):  # noqa: F811
         check(bsq, z, 4, bias=b, score=score, renormalize=renorm, **g)
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,groups", [(16, 4), (160, 8), (512, 16)])
+def test_sums_of_two_saturated_scores(bsq, E, groups, renorm):  # noqa: F811
+    """Sigmoid scores that are 1 in 32 or in 64 bits, 0, or masked, without a bias: groups go by the
+    sums in 64 bits, equal ones by their number, and the experts in them by their logits."""
+    inf, nan = np.inf, np.nan
+    rng = np.random.default_rng(E)
+    z = rng.standard_normal((14, E))
+    z[0] = 60 + 5 * z[0]                             # 1 in 64 bits: the first groups
+    z[1] = 20 + 2 * z[1]                             # 1 in 32 bits, told apart in 64
+    z[2] = 200 * z[2]
+    z[3] = 1e30 * np.sign(z[3]) * (1 + rng.random(E))
+    z[4, ::3] = inf
+    z[5, ::2] = nan
+    z[6, E // groups + 1:] = -inf                    # one group whole, the next with one expert
+    z[7, rng.random(E) < 0.8] = -inf
+    z[8] = -200 + 10 * z[8]                          # sums of 1e-87: 32 bits have none of them
+    z[9] = -900 + z[9]                               # 0 in 64 bits too
+    z[10] = np.where(np.arange(E) % 2, 50.0, -50.0) + z[10]
+    z[11], z[12] = -inf, nan
+    z[13, [1, E - 1]] = inf
+    for keep in (1, 2, groups - 1):
+        check(bsq, z, min(8, E // groups * keep), score="sigmoid", groups=groups, keep=keep, top=2, renormalize=renorm)
+
+
 @pytest.mark.parametrize("E", [16, 200, 400])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
