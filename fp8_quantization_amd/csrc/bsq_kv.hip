@@ -1059,10 +1059,7 @@ hipError_t attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) 
         else attend_rows<D, 4, MASKED>(a, grid, stream);
     } else if (p.block_cols == 32) {
         if constexpr (MASKED && D != 256) {
-            if (p.wide)
-                hipLaunchKernelGGL((attend_split_kernel<D, 2, 8, false, true>), grid, dim3(512), 0, stream, a);
-            else
-                hipLaunchKernelGGL((attend_split_kernel<D, 2, 4, false, true>), grid, dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((attend_split_kernel<D, 2, 4, false, true>), grid, dim3(256), 0, stream, a);
         } else {
             return hipErrorInvalidConfiguration;   // no plan of these kernels
         }
@@ -1122,7 +1119,10 @@ constexpr int64_t kRowsLeast = 4;
 // and 160 us, in blocks of 32 columns 54, 81, 105 and 192; trees of 48 tokens over 1500 .. 6000,
 // 32 heads on 8, of 4, 16 and 32: 43, 116 and 161, in blocks 38, 80 and 146).  Fewer take blocks
 // of 16 columns, or of 32 where there are kTwoBlocks of 16 (512: 36 and 38 us, 1024 of which the
-// second holds 4 columns: 124 and 102).  A tree has many pairs to join, so the pages are split
+// second holds 4 columns: 124 and 102), with four waves: eight, which are the faster for few blocks of
+// 16, are the slower here (in a graph, 64 trees of 8 tokens over 125 .. 500: 19.3 us, with eight waves
+// 28.7; over 1000 .. 4000: 71 and 75; 16 of 32 over those: 39 and 46; 64 of 8 with heads of 64: 12.6
+// and 20.7, 36 and 40).  A tree has many pairs to join, so the pages are split
 // only until there are kMaskedGroups workgroups (25 tokens over 20000, 56 workgroups: unsplit 67
 // us, in four 31, in twenty 31; 100 over 6000, 200 workgroups: 27, in two 37, in four 34).
 // Few columns of many pages are the form of many rows' again, its pages split: up to 80
@@ -1172,7 +1172,7 @@ AttendPlan plan_masked(int64_t num_heads, int64_t head_dim, int64_t num_q_heads,
         run = std::max(run, kSplitLeast);
     }
     p.splits = (int32_t)std::max<int64_t>((pages + run - 1) / run, 1);
-    if (!p.rows_form) p.wide = blocks * p.splits <= 512;
+    if (!p.rows_form) p.wide = p.block_cols == 16 && blocks * p.splits <= 512;
     p.threads = p.wide || (p.rows_form && head_dim == 256) ? 512 : 256;
     p.split_pages = (int32_t)run;
     return p;

@@ -170,7 +170,7 @@ def test_forms_of_many_sequences(bsq, D, seqs, n, heads, hq):  # noqa: F811
 @pytest.mark.parametrize("D,heads,hq", [(128, 8, 32), (64, 8, 32)])
 @pytest.mark.parametrize("seqs,n", [(64, 6), (48, 8), (32, 16)])
 def test_batches_of_small_trees(bsq, D, heads, hq, seqs, n):  # noqa: F811
-    """Blocks of 32 columns whose pages eight waves share; lengths in random order, some of one page
+    """Blocks of 32 columns, fewer than 512; lengths in random order, some of one page
     or without tokens before the tree."""
     rows = [n - s % 3 for s in range(seqs)]
     lens = [r + (s * 37 % 23) * 13 for s, r in enumerate(rows)]
