@@ -422,7 +422,8 @@ void logprobs(const LogprobArgs& a, hipStream_t stream) {
 // Elements of a thread and chunk.  Short ones, one chunk a workgroup, where a row fits (2000 rows of
 // 1000: 8.5 us, long 11.6) or where long ones would leave few workgroups; else long ones, several
 // a workgroup as long as there are kWorkgroups (2048 rows of 128000: 105 us, with 4096 workgroups
-// 119, 8192 140).
+// 119, 8192 140).  Chunks a workgroup are rounded down, so a row's last slice may be short: 2000 rows
+// are slices of 31 chunks and of one, 167 us in a graph where 2048, a slice each, take 112.
 constexpr int kLong = 16, kShort = 8;
 constexpr int64_t kWorkgroups = 2048;
 

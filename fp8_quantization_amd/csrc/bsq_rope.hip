@@ -219,8 +219,12 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
 // Steps of a wave: all of a row's where that gives waves enough for the CUs, else fewer, down to one
 // (16384 rows of 40 heads: 76 us with 10 steps a wave, 79 with five).
 constexpr int64_t kWavesWanted = 4096;
-// Inputs larger than the memory-side cache are read past the caches (336 MB read and written: 71
-// us, through them 77); smaller ones may lie there still (84 MB: 27 and 21).
+// Calls whose inputs and outputs together are larger than the memory-side cache read the inputs past
+// the caches.  Rows just written, past the caches and through them: BF16, 130 MB of input 56 us and
+// 55, 160 MB 66 and 68, 220 MB 88 and 105; FP32, whose outputs are half as large, 60 MB 27 and 22,
+// 200 MB 77 and 57, 260 MB 89 and 90, 300 MB 98 and 117.  Rows that no longer lie there are read past
+// them the faster at any size (BF16, 160 MB: 74 and 95; FP32, 200 MB: 69 and 98), so the rule of one
+// size for both types loses in FP32 from 180 to 260 MB what it gains for such rows.
 constexpr int64_t kCached = 256 << 20;
 
 template <int L, bool F32, Pairs PAIRS>
